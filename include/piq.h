@@ -367,6 +367,130 @@ int piq_wait_selftest(uint64_t wait_ns, int* where_out, void* workspace, size_t 
 int piq_upper_factor_noalloc(const float* H, int64_t in, float damp, const int32_t* perm,
                              float* U, double* lambda_out, void* stream);
 
+/* ------------------------------------------------------- 8-bit serving layer
+ * What runs next to a quantized layer in 8 bits: a linear layer on int8 codes,
+ * a key/value cache held in int8, and attention over it.  (The pages name both
+ * as the neighbours of weight quantization: the plugsky.com table's 8-bit row
+ * and the gankinterview.cn page's KV-cache quantization; they give no formula.
+ * The definitions below are this library's own.)
+ *
+ * Quantizer of all three: over a set of values with largest magnitude amax,
+ *   scale = amax / 127,  inverse = 1 / scale,
+ *   code = clip(rint(x * inverse), -127, 127)   (ties to even),
+ * every operation rounded to fp32.  A scale below 2^-126 is stored as 0 and its
+ * codes are 0.  A set that holds an infinity or NaN gets scale NaN and codes 0,
+ * so everything computed from it is NaN.
+ *
+ * Conventions of these entries, besides the ones above: `dtype` is the type of
+ * the unquantized tensors; row strides (ld*) are in elements; the calls only
+ * enqueue and never synchronize, so they can be captured into a graph, and no
+ * two of them share state except the buffers they are given.  `status` is a
+ * device int32[2] or NULL: what the device finds wrong (a page number or a
+ * length out of range, a wait that gave up) is recorded there as {PIQ_ERR_*, detail}, the
+ * first one staying until the caller clears it; either way no access leaves
+ * its buffer, and what depends on the bad value is skipped (writes) or NaN
+ * (results). */
+enum piq_dtype { PIQ_BF16 = 0, PIQ_FP16 = 1, PIQ_FP32 = 2 };
+
+/* Rows to int8, one scale a row: the tokens of X, or the output channels of W.
+ *   X       device [rows, cols], row stride ldx; 16-byte aligned, ldx and cols
+ *           multiples of 8.
+ *   codes   device int8 [rows, cols], row stride ldc >= cols, a multiple of 8,
+ *           8-byte aligned.
+ *   scales  device fp32 [rows].
+ * rows >= 0; 8 <= cols <= 2^20. */
+int piq_int8_quantize_rows(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ldx,
+                           int8_t* codes, int64_t ldc, float* scales, void* stream);
+
+/* Linear layer on int8 codes: with qx, sx the codes and scales of the rows of X
+ * (piq_int8_quantize_rows, done inside the call),
+ *   Y[t, c] = (sum_k qx[t, k] W[c, k]) * sx[t] * w_scale[c] + bias[c],
+ * the sum exact in int32, the rest in fp32, rounded once to dtype.
+ *   X        device [tokens, in], row stride ldx (multiple of 8), 16-byte aligned.
+ *   W        device int8 [out, in], row stride ldw (multiple of 16), 16-byte aligned.
+ *   w_scale  device fp32 [out].   bias  device fp32 [out] or NULL.
+ *   Y        device [tokens, out] of X's dtype, row stride ldy >= out.
+ * tokens >= 0; in % 8 == 0, 8 <= in <= 131064 (the int32 sums stay exact for
+ * every code, -128 among them); 1 <= out <= 2^24.
+ * Workspace: piq_int8_linear_workspace_bytes. */
+int piq_int8_linear_workspace_bytes(int64_t tokens, int64_t out, int64_t in, size_t* bytes);
+int piq_int8_linear(const void* X, int dtype, int64_t tokens, int64_t in, int64_t ldx,
+                    const int8_t* W, int64_t out, int64_t ldw, const float* w_scale,
+                    const float* bias, void* Y, int64_t ldy, int32_t* status, void* workspace,
+                    size_t ws_bytes, void* stream);
+
+/* The paged 8-bit key/value cache, shared by the next entries.
+ *   k_codes, v_codes  device int8 [pages, kv_heads, block, head_dim], contiguous:
+ *                     one block of tokens of one head is one run of bytes.
+ *   k_scale, v_scale  device fp32 [pages, kv_heads]: one scale for each block
+ *                     of tokens and head.
+ *   block_table       device int32 [batch, table_width], row stride ldt: the
+ *                     page that holds tokens [j block, (j + 1) block) of
+ *                     sequence b is block_table[b, j].
+ * head_dim is 64 or 128; block is 16, 32, 64 or 128; 1 <= kv_heads <= 1024;
+ * 1 <= batch <= 65535; 1 <= pages <= 2^31 - 1. Rows of ragged tensors belong to
+ * sequences by cu (device int32 [batch + 1], non-decreasing): rows cu[b] ..
+ * cu[b + 1] - 1 are sequence b's, in order; rows of no sequence are not touched.
+ *
+ * piq_kv8_append quantizes new tokens as it writes them.  Sequence b has
+ * lens_before[b] tokens in the cache and gets the rows cu_new[b] .. of k and v
+ * behind them.  The values of a block and head share one scale: for a block
+ * whose first token is written by this call, the quantizer's scale of its new
+ * values; for one that already holds tokens, the larger of that and the scale
+ * it has, and where the scale grows the codes c already there become
+ * rint(c * (old / new)).  A page that is written belongs to one sequence (a
+ * page two sequences share is read only); its positions behind the last token
+ * are left as they are.
+ *   k, v   device [tokens, kv_heads, head_dim], token strides ldk, ldv
+ *          (multiples of 8), 16-byte aligned.
+ *
+ * piq_kv8_read reads tokens back: row cu_rows[b] + i of k_out and v_out gets
+ * code * scale of sequence b's token start[b] + i, rounded to dtype.
+ *   k_out, v_out  device [rows, kv_heads, head_dim], token strides ldk, ldv. */
+int piq_kv8_append(const void* k, const void* v, int dtype, int64_t tokens, int64_t ldk,
+                   int64_t ldv, const int32_t* cu_new, const int32_t* lens_before, int64_t batch,
+                   const int32_t* block_table, int64_t table_width, int64_t ldt, int8_t* k_codes,
+                   int8_t* v_codes, float* k_scale, float* v_scale, int64_t pages, int kv_heads,
+                   int head_dim, int block, int32_t* status, void* stream);
+int piq_kv8_read(const int8_t* k_codes, const int8_t* v_codes, const float* k_scale,
+                 const float* v_scale, int64_t pages, int kv_heads, int head_dim, int block,
+                 const int32_t* cu_rows, const int32_t* start, int64_t batch,
+                 const int32_t* block_table, int64_t table_width, int64_t ldt, int64_t rows,
+                 void* k_out, void* v_out, int dtype, int64_t ldk, int64_t ldv, int32_t* status,
+                 void* stream);
+
+/* Causal attention of new tokens over the cache (which holds them already):
+ * sequence b has lens[b] tokens in the cache, the last cu_q[b + 1] - cu_q[b] of
+ * them are the rows of q.  Query head i reads head i / (heads / kv_heads).  A
+ * query at position p sees keys j <= p, and j > p - window when window > 0:
+ *   out = sum_j softmax_j(scale q . (k_scale k_j)) v_scale v_j,
+ *   lse = log sum_j exp(scale q . (k_scale k_j)).
+ * A query that sees no key gets out = 0 and lse = -infinity.
+ *   q, out  device [tokens, heads, head_dim], bf16 or fp16, token strides ldq
+ *           and ldo (multiples of 8), 16-byte aligned.
+ *   lse     device fp32 [tokens, heads] or NULL.
+ *   max_new, max_len   host upper bounds of the new tokens and of lens over the
+ *           batch: they size the launch and the workspace (a sequence above
+ *           them is an error: its rows are NaN).
+ *           max_len <= 2^26.
+ *   heads   a multiple of kv_heads, at most 256 kv_heads; tokens <= 2^24.
+ * Queries of bf16 are scaled by a power of two a row and used in fp16, exact for
+ * values down to 2^-14 of the row's largest; probabilities are used in fp16
+ * times 2^7, relative to the largest v_scale and probability in sight.  Sums
+ * and softmax statistics are fp32.
+ * Workspace: piq_kv8_attention_workspace_bytes with the same sizes. */
+int piq_kv8_attention_workspace_bytes(int64_t tokens, int heads, int kv_heads, int head_dim,
+                                      int64_t batch, int64_t max_new, int64_t max_len,
+                                      int window, size_t* bytes);
+int piq_kv8_attention(const void* q, int dtype, int64_t tokens, int64_t ldq, int heads,
+                      const int32_t* cu_q, const int32_t* lens, int64_t batch,
+                      const int32_t* block_table, int64_t table_width, int64_t ldt,
+                      const int8_t* k_codes, const int8_t* v_codes, const float* k_scale,
+                      const float* v_scale, int64_t pages, int kv_heads, int head_dim, int block,
+                      float scale, int window, int64_t max_new, int64_t max_len, void* out,
+                      int64_t ldo, float* lse, int32_t* status, void* workspace,
+                      size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

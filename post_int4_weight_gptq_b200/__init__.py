@@ -100,6 +100,23 @@ SIGNATURES = {
                                    _vp]),
     "piq_upper_factor_noalloc": (_c_int, [_vp, _c_i64, _c_float, _vp, _vp,
                                           ctypes.POINTER(ctypes.c_double), _vp]),
+    "piq_int8_quantize_rows": (_c_int, [_vp, _c_int, _c_i64, _c_i64, _c_i64, _vp, _c_i64, _vp,
+                                        _vp]),
+    "piq_int8_linear_workspace_bytes": (_c_int, [_c_i64, _c_i64, _c_i64, _c_size_p]),
+    "piq_int8_linear": (_c_int, [_vp, _c_int, _c_i64, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _vp,
+                                 _vp, _vp, _c_i64, _vp, _vp, ctypes.c_size_t, _vp]),
+    "piq_kv8_append": (_c_int, [_vp, _vp, _c_int, _c_i64, _c_i64, _c_i64, _vp, _vp, _c_i64, _vp,
+                                _c_i64, _c_i64, _vp, _vp, _vp, _vp, _c_i64, _c_int, _c_int,
+                                _c_int, _vp, _vp]),
+    "piq_kv8_read": (_c_int, [_vp, _vp, _vp, _vp, _c_i64, _c_int, _c_int, _c_int, _vp, _vp,
+                              _c_i64, _vp, _c_i64, _c_i64, _c_i64, _vp, _vp, _c_int, _c_i64,
+                              _c_i64, _vp, _vp]),
+    "piq_kv8_attention_workspace_bytes": (_c_int, [_c_i64, _c_int, _c_int, _c_int, _c_i64, _c_i64,
+                                                   _c_i64, _c_int, _c_size_p]),
+    "piq_kv8_attention": (_c_int, [_vp, _c_int, _c_i64, _c_i64, _c_int, _vp, _vp, _c_i64, _vp,
+                                   _c_i64, _c_i64, _vp, _vp, _vp, _vp, _c_i64, _c_int, _c_int,
+                                   _c_int, _c_float, _c_int, _c_i64, _c_i64, _vp, _c_i64, _vp,
+                                   _vp, _vp, ctypes.c_size_t, _vp]),
 }
 
 _lib = None
@@ -495,3 +512,275 @@ def upper_factor_noalloc(H, damp=0.01, perm=None, stream=None):
                                         ctypes.byref(lam), _stream(stream)),
            "piq_upper_factor_noalloc")
     return U, lam.value
+
+
+# ------------------------------------------------------------- 8-bit serving layer
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _rows_of(t, name, ndim, dtypes=_DTYPES):
+    """Checks a tensor of rows: on the GPU, of a type the entry takes, every
+    row (all but the first dimension) contiguous.  The row stride in elements."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has an unsupported dtype: {t.dtype}")
+    if t.ndim != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions, got {t.ndim}")
+    shape, stride = t.shape, t.stride()
+    want = 1
+    for i in range(ndim - 1, 0, -1):
+        if shape[i] > 1 and stride[i] != want and shape[0]:
+            raise ValueError(f"the rows of {name} must be contiguous")
+        want *= shape[i]
+    return stride[0] if shape[0] > 1 else max(stride[0], want)
+
+
+def _flat(t, dtype, name, ndim, shape=None):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.ndim != ndim or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {ndim} dimensions")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _same_device(dev, *tensors):
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on different devices: {t.device} and {dev}")
+
+
+class _On:
+    """The device and stream of one call: the tensors' device made current, and
+    memory that the call allocates taken from the stream it runs on."""
+    __slots__ = ("dev", "stream", "guards")
+
+    def __init__(self, dev, stream):
+        self.dev, self.stream, self.guards = dev, stream, ()
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.dev.index:
+            g = torch.cuda.device(self.dev)
+            g.__enter__()
+            self.guards = (g,)
+        cur = torch.cuda.current_stream()
+        if self.stream is not None and self.stream.cuda_stream != cur.cuda_stream:
+            g = torch.cuda.stream(self.stream)
+            g.__enter__()
+            self.guards += (g,)
+            cur = self.stream
+        return cur.cuda_stream
+
+    def __exit__(self, *a):
+        for g in reversed(self.guards):
+            g.__exit__(*a)
+
+
+def _status_ptr(status, dev):
+    if status is None:
+        return None
+    _flat(status, torch.int32, "status", 1)
+    if status.numel() < 2:
+        raise ValueError("status must hold two int32 values")
+    _same_device(dev, status)
+    return status.data_ptr()
+
+
+def _work(nbytes, dev, workspace):
+    """The caller's workspace if it is large enough, else a new one."""
+    if workspace is None or workspace.numel() < nbytes:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _flat(workspace, torch.uint8, "workspace", 1)
+    _same_device(dev, workspace)
+    return workspace
+
+
+def new_status(device=None):
+    """Two int32 words {code, detail} for the 8-bit entries, cleared."""
+    return torch.zeros(2, dtype=torch.int32, device=device or "cuda")
+
+
+def check_status(status, where="8-bit call"):
+    """Raises PiqError if an entry recorded an error in `status` (synchronizes),
+    and clears it."""
+    code = int(status[0])
+    if code != PIQ_OK:
+        status.zero_()
+        raise PiqError(code, where)
+
+
+def int8_quantize_rows(X, stream=None):
+    """(codes, scales): every row of X [rows, cols] (bf16, fp16 or fp32) as int8
+    codes with one fp32 scale; the tokens of an activation or the channels of a
+    weight.  The row stride of the codes is padded to 16."""
+    lib = load_library()
+    ldx = _rows_of(X, "X", 2)
+    rows, cols = X.shape
+    with _On(X.device, stream) as s:
+        codes = torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.int8,
+                            device=X.device)[:, :cols]
+        scales = torch.empty(rows, dtype=torch.float32, device=X.device)
+        _check(lib.piq_int8_quantize_rows(X.data_ptr(), _DTYPES[X.dtype], rows, cols, ldx,
+                                          codes.data_ptr(), (cols + 15) // 16 * 16,
+                                          scales.data_ptr(), s), "piq_int8_quantize_rows")
+    return codes, scales
+
+
+def int8_linear_workspace_bytes(tokens, out, inp) -> int:
+    return _query(load_library().piq_int8_linear_workspace_bytes, tokens, out, inp)
+
+
+def int8_linear(X, W, w_scale, bias=None, out=None, stream=None, workspace=None, status=None):
+    """X W^T + bias on int8 codes: the tokens X [tokens, in] (bf16, fp16, fp32)
+    are quantized inside the call, W [out, in] int8 and w_scale fp32 [out] are
+    int8_quantize_rows of the weight (row stride a multiple of 16), bias is fp32
+    [out].  The result has X's dtype."""
+    lib = load_library()
+    ldx = _rows_of(X, "X", 2)
+    ldw = _rows_of(W, "W", 2, (torch.int8,))
+    tokens, inp = X.shape
+    n = W.shape[0]
+    if W.shape[1] != inp:
+        raise ValueError("W and X disagree on the input dimension")
+    dev = X.device
+    _flat(w_scale, torch.float32, "w_scale", 1, (n,))
+    if bias is not None:
+        _flat(bias, torch.float32, "bias", 1, (n,))
+    _same_device(dev, W, w_scale, bias, out)
+    with _On(dev, stream) as s:
+        if out is None:
+            out = torch.empty((tokens, n), dtype=X.dtype, device=dev)
+            ldy = n
+        else:
+            ldy = _rows_of(out, "out", 2, (X.dtype,))
+            if tuple(out.shape) != (tokens, n):
+                raise ValueError(f"out must have shape {(tokens, n)}")
+        ws = _work(int8_linear_workspace_bytes(tokens, n, inp), dev, workspace)
+        _check(lib.piq_int8_linear(X.data_ptr(), _DTYPES[X.dtype], tokens, inp, ldx, W.data_ptr(),
+                                   n, ldw, w_scale.data_ptr(),
+                                   None if bias is None else bias.data_ptr(), out.data_ptr(), ldy,
+                                   _status_ptr(status, dev), ws.data_ptr(), ws.numel(), s),
+               "piq_int8_linear")
+    return out
+
+
+#: The 8-bit paged cache: codes int8 [pages, kv_heads, block, head_dim], scales
+#: fp32 [pages, kv_heads] (one for each block of tokens and head).
+KV8Cache = collections.namedtuple("KV8Cache", "k v k_scale v_scale")
+
+
+def kv8_cache(pages, kv_heads, head_dim, block=64, device=None):
+    """An empty KV8Cache of `pages` pages of `block` tokens."""
+    dev = torch.device(device or "cuda")
+    shape = (pages, kv_heads, block, head_dim)
+    return KV8Cache(torch.zeros(shape, dtype=torch.int8, device=dev),
+                    torch.zeros(shape, dtype=torch.int8, device=dev),
+                    torch.zeros(shape[:2], dtype=torch.float32, device=dev),
+                    torch.zeros(shape[:2], dtype=torch.float32, device=dev))
+
+
+def _kv8(cache, cu, lens, block_table):
+    """Checks a cache and its ragged batch: (device, cache arguments of the C
+    call, batch, table arguments)."""
+    k, v, ks, vs = cache
+    _flat(k, torch.int8, "cache.k", 4)
+    shape = tuple(k.shape)
+    _flat(v, torch.int8, "cache.v", 4, shape)
+    _flat(ks, torch.float32, "cache.k_scale", 2, shape[:2])
+    _flat(vs, torch.float32, "cache.v_scale", 2, shape[:2])
+    ldt = _rows_of(block_table, "block_table", 2, (torch.int32,))
+    batch, width = block_table.shape
+    _flat(cu, torch.int32, "cu", 1, (batch + 1,))
+    _flat(lens, torch.int32, "lengths", 1, (batch,))
+    dev = k.device
+    _same_device(dev, v, ks, vs, block_table, cu, lens)
+    return (dev, (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape[0], shape[1],
+                  shape[3], shape[2]), batch, (block_table.data_ptr(), width, ldt))
+
+
+def kv8_append(cache, k, v, cu, lens_before, block_table, stream=None, status=None):
+    """Quantizes new keys and values k, v [tokens, kv_heads, head_dim] (bf16,
+    fp16, fp32; token strides free, so slices of a fused projection do) into the
+    cache behind the lens_before [batch] tokens each sequence has there; rows
+    cu[b] .. cu[b + 1] - 1 are sequence b's."""
+    lib = load_library()
+    dev, c, batch, table = _kv8(cache, cu, lens_before, block_table)
+    ldk, ldv = _rows_of(k, "k", 3), _rows_of(v, "v", 3, (k.dtype,))
+    if k.shape != v.shape or tuple(k.shape[1:]) != (c[5], c[6]):
+        raise ValueError("k and v must be [tokens, kv_heads, head_dim] of the cache")
+    _same_device(dev, k, v)
+    with _On(dev, stream) as s:
+        _check(lib.piq_kv8_append(k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], k.shape[0], ldk,
+                                  ldv, cu.data_ptr(), lens_before.data_ptr(), batch, *table, *c,
+                                  _status_ptr(status, dev), s), "piq_kv8_append")
+
+
+def kv8_read(cache, cu, start, block_table, rows, dtype=torch.bfloat16, out=None, stream=None,
+             status=None):
+    """(k, v) [rows, kv_heads, head_dim]: row cu[b] + i is sequence b's cached
+    token start[b] + i.  Rows of no sequence are left as they are (`out`, a pair
+    of tensors) or undefined."""
+    lib = load_library()
+    dev, c, batch, table = _kv8(cache, cu, start, block_table)
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype: {dtype}")
+    shape = (rows, c[5], c[6])
+    with _On(dev, stream) as s:
+        if out is None:
+            out = (torch.empty(shape, dtype=dtype, device=dev),
+                   torch.empty(shape, dtype=dtype, device=dev))
+        k, v = out
+        ldk, ldv = _rows_of(k, "k", 3, (dtype,)), _rows_of(v, "v", 3, (dtype,))
+        if tuple(k.shape) != shape or tuple(v.shape) != shape:
+            raise ValueError(f"out must be two tensors of shape {shape}")
+        _same_device(dev, k, v)
+        _check(lib.piq_kv8_read(*c, cu.data_ptr(), start.data_ptr(), batch, *table, rows,
+                                k.data_ptr(), v.data_ptr(), _DTYPES[dtype], ldk, ldv,
+                                _status_ptr(status, dev), s), "piq_kv8_read")
+    return k, v
+
+
+def kv8_attention_workspace_bytes(tokens, heads, kv_heads, head_dim, batch, max_new, max_len,
+                                  window=0) -> int:
+    return _query(load_library().piq_kv8_attention_workspace_bytes, tokens, heads, kv_heads,
+                  head_dim, batch, max_new, max_len, window)
+
+
+def kv8_attention(cache, q, cu, lens, block_table, max_new, max_len, scale=None, window=0,
+                  return_lse=False, out=None, stream=None, workspace=None, status=None):
+    """Causal attention of q [tokens, heads, head_dim] (bf16 or fp16) over the
+    cache: sequence b's rows cu[b] .. cu[b + 1] - 1 are the last of its lens[b]
+    cached tokens (appended before this call).  max_new and max_len bound the
+    rows and lens of every sequence; scale defaults to head_dim ** -0.5; window
+    > 0 limits a query to the last `window` keys.  Returns out, or (out, lse)
+    with lse fp32 [tokens, heads]."""
+    lib = load_library()
+    dev, c, batch, table = _kv8(cache, cu, lens, block_table)
+    ldq = _rows_of(q, "q", 3, (torch.bfloat16, torch.float16))
+    tokens, heads, d = q.shape
+    if d != c[6]:
+        raise ValueError("q and the cache disagree on head_dim")
+    _same_device(dev, q, out)
+    with _On(dev, stream) as s:
+        if out is None:
+            out = torch.empty((tokens, heads, d), dtype=q.dtype, device=dev)
+            ldo = heads * d
+        else:
+            ldo = _rows_of(out, "out", 3, (q.dtype,))
+            if out.shape != q.shape:
+                raise ValueError(f"out must have shape {tuple(q.shape)}")
+        lse = (torch.empty((tokens, heads), dtype=torch.float32, device=dev)
+               if return_lse else None)
+        ws = _work(kv8_attention_workspace_bytes(tokens, heads, c[5], d, batch, max_new, max_len,
+                                                 window), dev, workspace)
+        _check(lib.piq_kv8_attention(q.data_ptr(), _DTYPES[q.dtype], tokens, ldq, heads,
+                                     cu.data_ptr(), lens.data_ptr(), batch, *table, *c,
+                                     float(d ** -0.5 if scale is None else scale), window,
+                                     max_new, max_len, out.data_ptr(), ldo,
+                                     None if lse is None else lse.data_ptr(),
+                                     _status_ptr(status, dev), ws.data_ptr(), ws.numel(), s),
+               "piq_kv8_attention")
+    return (out, lse) if return_lse else out

@@ -1,0 +1,681 @@
+// Attention of new tokens over the 8-bit paged cache, a chunk of keys at a time.
+//
+//   x_j = scale q . (k_scale k_j),  out = sum_j 2^(x_j') v_scale v_j / sum_j 2^(x_j')
+//
+// (x' = x log2 e - running maximum).  The codes go from memory to registers in
+// 16-byte loads, laid out so that they already are matrix fragments: the order
+// of the dimensions inside a fragment is free as long as q's agrees, so lane
+// (r, c) = (lane / 4, lane % 4) takes bytes 16 c .. of token r for the scores
+// and bytes r * head_dim / 8 .. of tokens 2c, 2c + 1, 2c + 8, 2c + 9 for the
+// values.  Nothing is staged in shared memory.  A byte becomes a half exactly:
+// (code + 128) under the exponent of 1024 is 1152 + code, minus 1152.
+//
+// Keys and values are the wide operand (16 tokens, or 16 dimensions, a
+// product), the queries the narrow one (8 rows), because a decoding step has
+// few rows for every key: S^T = K q^T and O^T = V^T P^T, with P^T's fragment
+// made from S^T's by an 8x8 transpose in registers.
+//
+// Probabilities enter the second product in fp16 as 2^7 p v_scale / (largest
+// v_scale so far), p relative to a running maximum that moves only when a score
+// exceeds it by 2^8: at most 2^15, and what is more than 2^31 below the largest
+// is lost.  The sum of p stays in fp32.
+#include <algorithm>
+
+#include "serve.h"
+
+namespace piq {
+
+struct Kv8Attn {
+  const void* q;
+  int64_t tokens, ldq;
+  const int32_t *cu, *lens;
+  const int32_t* table;
+  int64_t width, ldt;
+  const int8_t *kc, *vc;
+  const float *ks, *vs;
+  int64_t pages;
+  int batch, heads, kv_heads, block, group;  // group = heads / kv_heads
+  float scale2;                              // scale * log2(e)
+  int64_t window;                            // 0: none
+  int64_t max_new, max_len;
+  int64_t chunk;                             // keys a CTA, a multiple of 128
+  int chunks;                                // most chunks of a sequence
+  void* out;
+  int64_t ldo;
+  float* lse;
+  float* part_o;   // [chunks][tokens][heads][D] when chunks > 1
+  float2* part_ml; // [chunks][tokens][heads]: running maximum (log2), sum
+  int32_t* status;
+};
+
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLow = -3.0e38f;      // below every score: "no key yet"
+constexpr float kPScale = 128.0f;     // 2^7
+constexpr float kSlack = 8.0f;        // log2 by which a score may pass the maximum
+constexpr int kWarps = 8;
+constexpr int kMaxPages = 256;        // pages of a chunk (4096 keys, blocks of 16)
+
+// Keys that some query of the sequence sees: [first, len).
+__device__ __forceinline__ int64_t first_key(int64_t len, int64_t n, int64_t window) {
+  return window > 0 ? max(static_cast<int64_t>(0), len - n + 1 - window) : 0;
+}
+
+__device__ __forceinline__ void halves_of(uint32_t w, uint32_t& even, uint32_t& odd) {
+  // bytes 0 and 2, bytes 1 and 3, each + 128 under 0x6400, minus 1152
+  const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+  const uint32_t e = (w & 0x00FF00FFu) ^ 0x64806480u;
+  const uint32_t o = ((w >> 8) & 0x00FF00FFu) ^ 0x64806480u;
+  const __half2 eh = __hsub2(*reinterpret_cast<const __half2*>(&e), off);
+  const __half2 oh = __hsub2(*reinterpret_cast<const __half2*>(&o), off);
+  even = *reinterpret_cast<const uint32_t*>(&eh);
+  odd = *reinterpret_cast<const uint32_t*>(&oh);
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <typename T>
+__device__ __forceinline__ float to_float(T x);
+template <>
+__device__ __forceinline__ float to_float<__half>(__half x) { return __half2float(x); }
+template <>
+__device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 x) {
+  return __bfloat162float(x);
+}
+
+// A row of q in fp16 and the factor that undoes its scaling.  bf16 rows are
+// scaled by the power of two that brings their largest magnitude into [1, 2).
+template <typename T>
+__device__ __forceinline__ float row_exponent(float amax, float& mul);
+template <>
+__device__ __forceinline__ float row_exponent<__half>(float amax, float& mul) {
+  mul = 1.0f;
+  return amax < __uint_as_float(0x7F800000u) ? 1.0f : __uint_as_float(0x7FC00000u);
+}
+template <>
+__device__ __forceinline__ float row_exponent<__nv_bfloat16>(float amax, float& mul) {
+  const uint32_t e = __float_as_uint(amax) >> 23;  // biased exponent
+  if (e == 255u || !(amax == amax)) {
+    mul = 0.0f;
+    return __uint_as_float(0x7FC00000u);
+  }
+  if (e < 2u || e > 252u) {  // mul and its inverse stay normal numbers
+    const bool big = e > 252u;
+    mul = big ? 0x1p-126f : 0x1p126f;
+    return big ? 0x1p126f : 0x1p-126f;
+  }
+  mul = __uint_as_float((254u - e) << 23);
+  return __uint_as_float(e << 23);
+}
+
+// NT groups of eight query rows of one kv head (rows are (token, head) pairs,
+// the heads of the group fastest) against one chunk of keys.
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel(Kv8Attn p) {
+  constexpr int ROWS = 8 * NT;
+  constexpr int KS = D / 16;   // k steps of the scores = 16-row tiles of the output
+  constexpr int KV = D / 64;   // 16-byte loads of a key a lane; value loads are 4 of D / 8 bytes
+  constexpr int OLD = D + 4;   // row stride of the joined output in shared memory
+  __shared__ int s_page[kMaxPages];
+  __shared__ float s_ks[kMaxPages], s_vs[kMaxPages];
+  __shared__ __align__(16) __half s_q[ROWS][D];
+  __shared__ float s_rs[ROWS];
+  __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
+  __shared__ float s_o[kWarps / 2][ROWS][OLD];
+
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = lane >> 2, c = lane & 3;
+  const int b = blockIdx.z;
+  const int row_groups = static_cast<int>(gridDim.x) / p.kv_heads;
+  const int kvh = blockIdx.x / row_groups, rg = blockIdx.x % row_groups;
+  const int part = blockIdx.y;
+  const int64_t q0 = __ldg(p.cu + b), q1 = __ldg(p.cu + b + 1), len = __ldg(p.lens + b);
+  const int64_t n = q1 - q0;
+  if (n == 0) return;
+  T* out = static_cast<T*>(p.out);
+  if (q0 < 0 || n < 0 || q1 > p.tokens || n > p.max_new || len < n || len > p.max_len ||
+      len > p.width * p.block) {
+    // lengths that cannot be: the sequence's rows, as far as they exist, are NaN
+    if (blockIdx.x != 0 || part != 0) return;
+    if (threadIdx.x == 0) note_status(p.status, PIQ_ERR_INVALID_ARG, b);
+    const int64_t t0 = max(q0, static_cast<int64_t>(0)), t1 = min(q1, p.tokens);
+    const float nan = __uint_as_float(0x7FC00000u);
+    for (int64_t t = t0; t < t1; ++t) {
+      for (int i = threadIdx.x; i < p.heads * D; i += blockDim.x)
+        out[t * p.ldo + i] = from_float<T>(nan);
+      if (p.lse != nullptr)
+        for (int i = threadIdx.x; i < p.heads; i += blockDim.x) p.lse[t * p.heads + i] = nan;
+    }
+    return;
+  }
+  const int64_t rows = n * p.group;
+  const int64_t row0 = static_cast<int64_t>(rg) * ROWS;
+  if (row0 >= rows) return;
+  // keys of this chunk: chunks are counted from the block of the first key in sight
+  const int64_t first = first_key(len, n, p.window);
+  const int64_t origin = first / p.block * p.block;
+  const int64_t k0 = origin + part * p.chunk;
+  if (k0 >= len) return;
+  const int64_t k1 = min(k0 + p.chunk, len);
+  const bool single = len - origin <= p.chunk;  // this CTA has all the sequence's keys
+
+  // -------------------------------------------------- pages and scales, queries
+  const int npages = static_cast<int>(k1 > k0 ? (k1 - k0 + p.block - 1) / p.block : 0);
+  for (int i = threadIdx.x; i < npages; i += blockDim.x) {
+    int pg = __ldg(p.table + b * p.ldt + k0 / p.block + i);
+    float ks = __uint_as_float(0x7FC00000u), vs = ks;
+    if (pg >= 0 && pg < p.pages) {
+      ks = __ldg(p.ks + static_cast<int64_t>(pg) * p.kv_heads + kvh);
+      vs = __ldg(p.vs + static_cast<int64_t>(pg) * p.kv_heads + kvh);
+    } else {
+      note_status(p.status, PIQ_ERR_INVALID_ARG, b);
+      pg = 0;
+    }
+    s_page[i] = pg;
+    s_ks[i] = ks;
+    s_vs[i] = vs;
+  }
+  for (int i = warp; i < ROWS; i += kWarps) {
+    const int64_t row = row0 + i;
+    float v[D / 32];
+    float amax = 0.0f;
+    bool nan = false;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      v[j] = 0.0f;
+      if (row < rows) {
+        const int64_t t = q0 + row / p.group;
+        const int head = kvh * p.group + static_cast<int>(row % p.group);
+        v[j] = to_float(static_cast<const T*>(p.q)[t * p.ldq + head * D + 32 * j + lane]);
+      }
+      amax = fmaxf(amax, fabsf(v[j]));
+      nan |= !(v[j] == v[j]);
+    }
+    amax = warp_max(amax);
+    if (__any_sync(0xffffffffu, nan)) amax = __uint_as_float(0x7FC00000u);
+    float mul;
+    const float undo = row_exponent<T>(amax, mul);
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      const float h = undo == undo ? v[j] * mul : 0.0f;
+      s_q[i][32 * j + lane] = __float2half_rn(h);
+    }
+    if (lane == 0) s_rs[i] = undo * p.scale2;
+  }
+  __syncthreads();
+
+  // -------------------------------------------------------------- fragments of q
+  uint32_t qf[NT][KS][2];
+  float rs[NT][2];
+  int64_t hi[NT][2];  // keys that rows 2c, 2c + 1 see: j < hi
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      // bytes 16 c + 4 w + {0, 2} and {1, 3} of each 64-byte half, w = s % 4
+      const uint2 x = *reinterpret_cast<const uint2*>(&s_q[8 * t + r][64 * (s / 4) + 16 * c + 4 * (s % 4)]);
+      qf[t][s][0] = __byte_perm(x.x, x.y, 0x5410);
+      qf[t][s][1] = __byte_perm(x.x, x.y, 0x7632);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int64_t row = row0 + 8 * t + 2 * c + e;
+      rs[t][e] = s_rs[8 * t + 2 * c + e];
+      hi[t][e] = row < rows ? len - n + row / p.group + 1 : 0;
+    }
+  }
+  // tiles in which every row sees every key need no masks
+  const int64_t last_row = min(row0 + ROWS, rows) - 1;
+  const int64_t all_lo = p.window > 0 ? len - n + last_row / p.group + 1 - p.window : 0;
+  const int64_t all_hi = row0 + ROWS <= rows ? len - n + row0 / p.group + 1 : 0;
+
+  float m[NT][2], l[NT][2], o[NT][KS][4];
+  float vmax = 0.0f;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    m[t][0] = m[t][1] = kLow;
+    l[t][0] = l[t][1] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < KS; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.0f;
+  }
+
+  // ------------------------------------------------------------- the keys, 16 a step
+  const int ntiles = static_cast<int>(k1 > k0 ? (k1 - k0 + 15) / 16 : 0);
+  const int tpb = p.block / 16;
+  uint4 kr[2][KV];
+  uint32_t vr[4][D / 32];
+  auto base_of = [&](int tile) {
+    return (static_cast<int64_t>(s_page[tile / tpb]) * p.kv_heads + kvh) * p.block * D +
+           (tile % tpb) * 16 * D;
+  };
+  auto load_k = [&](int tile) {
+    const int8_t* kb = p.kc + base_of(tile);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < KV; ++j)
+        kr[h][j] = __ldg(reinterpret_cast<const uint4*>(kb + (r + 8 * h) * D + 64 * j + 16 * c));
+  };
+  auto load_v = [&](int tile) {
+    const int8_t* vb = p.vc + base_of(tile);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const int8_t* at = vb + (2 * c + (h & 1) + 8 * (h >> 1)) * D + r * (D / 8);
+      if constexpr (D == 128) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(at));
+        vr[h][0] = x.x;
+        vr[h][1] = x.y;
+        vr[h][2] = x.z;
+        vr[h][3] = x.w;
+      } else {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(at));
+        vr[h][0] = x.x;
+        vr[h][1] = x.y;
+      }
+    }
+  };
+  if (warp < ntiles) {
+    load_k(warp);
+    load_v(warp);
+  }
+  for (int tile = warp; tile < ntiles; tile += kWarps) {
+    const int64_t key0 = k0 + 16 * tile;
+    float s[NT][4] = {};
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const uint4 w0 = kr[0][ks / 4], w1 = kr[1][ks / 4];
+      const uint32_t x0 = ks % 4 == 0 ? w0.x : ks % 4 == 1 ? w0.y : ks % 4 == 2 ? w0.z : w0.w;
+      const uint32_t x1 = ks % 4 == 0 ? w1.x : ks % 4 == 1 ? w1.y : ks % 4 == 2 ? w1.z : w1.w;
+      uint32_t a0, a1, a2, a3;
+      halves_of(x0, a0, a2);
+      halves_of(x1, a1, a3);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) mma_f16(s[t], a0, a1, a2, a3, qf[t][ks][0], qf[t][ks][1]);
+    }
+    const float kscale = s_ks[tile / tpb], vscale = s_vs[tile / tpb];
+    if (tile + kWarps < ntiles) load_k(tile + kWarps);
+
+    // scores in log2 units, masked
+    bool over = false;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[t][e] *= rs[t][e & 1] * kscale;
+      if (key0 < all_lo || key0 + 16 > all_hi) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int64_t j = key0 + r + 8 * (e >> 1), h = hi[t][e & 1];
+          const bool see = j < h && (p.window == 0 || j >= h - p.window);
+          if (!see) s[t][e] = __uint_as_float(0xFF800000u);
+        }
+      }
+      over |= fmaxf(s[t][0], s[t][2]) > m[t][0] + kSlack;
+      over |= fmaxf(s[t][1], s[t][3]) > m[t][1] + kSlack;
+    }
+    float fresh = vscale > vmax ? vscale : vmax;
+    if (__any_sync(0xffffffffu, over) || fresh != vmax) {
+      // the maximum (or the largest value scale) moves: what was summed is rescaled
+      const float fv = vmax > 0.0f ? vmax / fresh : 0.0f;
+      vmax = fresh;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(s[t][e], s[t][e + 2]);
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          const float nm = fmaxf(m[t][e], x);
+          f[e] = exp2_fast(m[t][e] - nm);
+          m[t][e] = nm;
+          l[t][e] *= f[e];
+          f[e] *= fv;
+        }
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+          o[t][j][0] *= f[0];
+          o[t][j][1] *= f[1];
+          o[t][j][2] *= f[0];
+          o[t][j][3] *= f[1];
+        }
+      }
+    }
+    // probabilities; those of the values carry the block's scale (NaN scales stay NaN,
+    // but only where a key is seen)
+    const float vf = vmax > 0.0f ? kPScale * (vscale / vmax) : (vscale == vscale ? 0.0f : vscale);
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float p0 = exp2_fast(s[t][2 * h] - m[t][0]);
+        const float p1 = exp2_fast(s[t][2 * h + 1] - m[t][1]);
+        l[t][0] += p0;
+        l[t][1] += p1;
+        const __half2 ph = __floats2half2_rn(p0 == 0.0f ? 0.0f : p0 * vf, p1 == 0.0f ? 0.0f : p1 * vf);
+        pb[t][h] = transpose8x8(*reinterpret_cast<const uint32_t*>(&ph));
+      }
+    }
+    // keys past the end of the page's tokens: their codes are whatever lies there, times 0
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+      // four dimensions of tokens (2c, 2c + 1) and (2c + 8, 2c + 9)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t sel = half == 0 ? 0x5410u : 0x7632u;  // d0 d1 | d2 d3 of both tokens
+        uint32_t a0, a1, a2, a3;
+        halves_of(__byte_perm(vr[0][w], vr[1][w], sel), a0, a1);
+        halves_of(__byte_perm(vr[2][w], vr[3][w], sel), a2, a3);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma_f16(o[t][2 * w + half], a0, a1, a2, a3, pb[t][0], pb[t][1]);
+      }
+    }
+    if (tile + kWarps < ntiles) load_v(tile + kWarps);
+  }
+
+  // --------------------------------------------------------------- join the warps
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 4);
+      l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 8);
+      l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 16);
+      if (r == 0) {
+        s_m[warp][8 * t + 2 * c + e] = m[t][e];
+        s_l[warp][8 * t + 2 * c + e] = l[t][e];
+      }
+    }
+  __syncthreads();
+  float f[NT][2];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float top = kLow;
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][8 * t + 2 * c + e]);
+      f[t][e] = exp2_fast(m[t][e] - top) * (vmax / kPScale);
+    }
+  // halves of the warps in turn, each adding into a buffer of its own
+  for (int pass = 0; pass < 2; ++pass) {
+    if (warp / (kWarps / 2) == pass) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < KS; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            // tile j holds dimensions r D / 8 + 2 j (rows 0 - 7) and + 2 j + 1 (rows 8 - 15)
+            float* at = &s_o[warp % (kWarps / 2)][8 * t + 2 * c + (e & 1)]
+                            [r * (D / 8) + 2 * j + (e >> 1)];
+            const float x = o[t][j][e] * f[t][e & 1];
+            *at = pass == 0 ? x : *at + x;
+          }
+    }
+    __syncthreads();
+  }
+  for (int i = warp; i < ROWS; i += kWarps) {
+    const int64_t row = row0 + i;
+    if (row >= rows) break;
+    float top = kLow, sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][i]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) sum += s_l[w][i] * exp2_fast(s_m[w][i] - top);
+    const int64_t t = q0 + row / p.group;
+    const int head = kvh * p.group + static_cast<int>(row % p.group);
+    const float norm = single ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
+    const int64_t slot = (static_cast<int64_t>(part) * p.tokens + t) * p.heads + head;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      float x = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps / 2; ++w) x += s_o[w][i][32 * j + lane];
+      x *= norm;
+      if (single)
+        out[t * p.ldo + head * D + 32 * j + lane] = from_float<T>(x);
+      else
+        p.part_o[slot * D + 32 * j + lane] = x;
+    }
+    if (lane == 0) {
+      if (!single)
+        p.part_ml[slot] = make_float2(top, sum);
+      else if (p.lse != nullptr)
+        p.lse[t * p.heads + head] =
+            sum == 0.0f ? __uint_as_float(0xFF800000u) : (top + log2f(sum)) * kLn2;
+    }
+  }
+}
+
+// Joins the chunks of one (token, head): the CTA's warps take chunks in turn.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) kv8_join_kernel(Kv8Attn p) {
+  __shared__ float s_top[4], s_sum[4];
+  __shared__ float s_o[4][D];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = blockIdx.x;
+  const int head = blockIdx.y;
+  const int b = find_sequence(p.cu, p.batch, t, lane);
+  if (b < 0) return;
+  const int64_t q0 = __ldg(p.cu + b), q1 = __ldg(p.cu + b + 1), len = __ldg(p.lens + b);
+  const int64_t n = q1 - q0;
+  if (q0 < 0 || q1 > p.tokens || n > p.max_new || len < n || len > p.max_len ||
+      len > p.width * p.block)
+    return;  // its rows are NaN already
+  const int64_t origin = first_key(len, n, p.window) / p.block * p.block;
+  const int nc = static_cast<int>((len - origin + p.chunk - 1) / p.chunk);
+  if (nc <= 1) return;  // written by its only chunk
+  const int64_t stride = p.tokens * p.heads;
+  const float2* ml = p.part_ml + t * p.heads + head;
+  const float* po = p.part_o + (t * p.heads + head) * D;
+  float top = kLow, sum = 0.0f, o[D / 32] = {};
+  for (int i = warp; i < nc; i += 4) {
+    const float2 x = ml[i * stride];
+    const float nt = fmaxf(top, x.x);
+    const float fo = exp2_fast(top - nt), fx = exp2_fast(x.x - nt);
+    top = nt;
+    sum = sum * fo + x.y * fx;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) o[j] = o[j] * fo + po[i * stride * D + 32 * j + lane] * fx;
+  }
+  if (lane == 0) {
+    s_top[warp] = top;
+    s_sum[warp] = sum;
+  }
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) s_o[warp][32 * j + lane] = o[j];
+  __syncthreads();
+  float all = kLow, total = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) all = fmaxf(all, s_top[w]);
+#pragma unroll
+  for (int w = 0; w < 4; ++w) total += s_sum[w] * exp2_fast(s_top[w] - all);
+  const float norm = total == 0.0f ? 0.0f : 1.0f / total;
+  for (int d = threadIdx.x; d < D; d += 128) {
+    float x = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) x += s_o[w][d] * exp2_fast(s_top[w] - all);
+    static_cast<T*>(p.out)[t * p.ldo + head * D + d] = from_float<T>(x * norm);
+  }
+  if (threadIdx.x == 0 && p.lse != nullptr)
+    p.lse[t * p.heads + head] =
+        total == 0.0f ? __uint_as_float(0xFF800000u) : (all + log2f(total)) * kLn2;
+}
+
+// Keys a chunk: enough CTAs for two waves of two a multiprocessor, but no
+// chunk so short that joining it costs more than it spreads.
+constexpr int64_t kMinChunk = 256, kMaxChunk = 4096;
+
+struct AttnPlan {
+  int nt;            // groups of eight rows a CTA
+  int64_t row_groups, chunk;
+  int chunks;
+};
+
+AttnPlan plan_attention(int64_t tokens, int heads, int kv_heads, int64_t batch, int64_t max_new, int64_t max_len,
+                        int64_t window) {
+  AttnPlan a;
+  const int64_t rows = std::min(max_new, tokens) * (heads / kv_heads);
+  a.nt = rows <= 8 ? 1 : 2;
+  a.row_groups = std::max<int64_t>(1, ceil_div(rows, 8 * a.nt));
+  int64_t span = max_len;  // most keys in sight of a sequence, from a block's (at most 128) start
+  if (window > 0) span = std::min(span, window + max_new + 128);
+  span = std::max<int64_t>(span, 1);
+  const int64_t ctas = a.row_groups * kv_heads * batch;
+  const int64_t want = std::max<int64_t>(1, 4 * 148 / ctas);
+  a.chunk = ceil_div(ceil_div(span, want), 128) * 128;
+  a.chunk = std::min(std::max(a.chunk, kMinChunk), kMaxChunk);
+  a.chunks = static_cast<int>(ceil_div(span, a.chunk));
+  return a;
+}
+
+bool attn_sizes_ok(int64_t tokens, int heads, int kv_heads, int head_dim, int64_t batch,
+                   int64_t max_new, int64_t max_len, int window) {
+  return tokens >= 0 && tokens <= (int64_t)1 << 24 && kv_heads >= 1 && kv_heads <= 1024 &&
+         heads >= kv_heads && heads % kv_heads == 0 && heads / kv_heads <= 256 && heads <= 65535 &&
+         (head_dim == 64 || head_dim == 128) && batch >= 1 && batch <= 65535 && max_new >= 0 &&
+         max_new <= INT32_MAX && max_len >= 0 && max_len <= (int64_t)1 << 26 && window >= 0;
+}
+
+struct AttnWs {
+  size_t ml_at, bytes;
+};
+AttnWs attn_ws(const AttnPlan& a, int64_t tokens, int heads, int head_dim) {
+  AttnWs w;
+  const size_t slots = a.chunks > 1 ? static_cast<size_t>(a.chunks) * tokens * heads : 0;
+  w.ml_at = (slots * head_dim * 4 + 255) / 256 * 256;
+  w.bytes = std::max<size_t>(256, w.ml_at + (slots * 8 + 255) / 256 * 256);
+  return w;
+}
+
+template <typename T, int D>
+int launch_attention(const Kv8Attn& p, const AttnPlan& a, cudaStream_t stream) {
+  void (*kern)(Kv8Attn) = a.nt == 1 ? kv8_chunk_kernel<T, D, 1> : kv8_chunk_kernel<T, D, 2>;
+  const unsigned gx = static_cast<unsigned>(a.row_groups * p.kv_heads);
+  note_launch();
+  if (launch_pdl(kern, dim3(gx, a.chunks, p.batch), dim3(32 * kWarps), 0,
+                 stream, p) != cudaSuccess)
+    return PIQ_ERR_CUDA;
+  if (a.chunks == 1) return PIQ_OK;
+  note_launch();
+  return launch_pdl(kv8_join_kernel<T, D>, dim3(static_cast<unsigned>(p.tokens), p.heads),
+                    dim3(128), 0, stream, p) == cudaSuccess
+             ? PIQ_OK
+             : PIQ_ERR_CUDA;
+}
+
+}  // namespace
+
+bool kv8_cache_ok(const void* kc, const void* vc, const void* ks, const void* vs, int64_t pages,
+                  int heads, int head_dim, int block);
+bool kv8_table_ok(const void* cu, const void* lens, int64_t batch, const void* table,
+                  int64_t width, int64_t ldt, const void* status);
+
+}  // namespace piq
+
+extern "C" {
+using namespace piq;
+
+int piq_kv8_attention_workspace_bytes(int64_t tokens, int heads, int kv_heads, int head_dim,
+                                      int64_t batch, int64_t max_new, int64_t max_len,
+                                      int window, size_t* bytes) {
+  if (bytes == nullptr ||
+      !attn_sizes_ok(tokens, heads, kv_heads, head_dim, batch, max_new, max_len, window))
+    return PIQ_ERR_INVALID_ARG;
+  const AttnPlan a = plan_attention(tokens, heads, kv_heads, batch, max_new, max_len, window);
+  *bytes = attn_ws(a, tokens, heads, head_dim).bytes;
+  return PIQ_OK;
+}
+
+int piq_kv8_attention(const void* q, int dtype, int64_t tokens, int64_t ldq, int heads,
+                      const int32_t* cu_q, const int32_t* lens, int64_t batch,
+                      const int32_t* block_table, int64_t table_width, int64_t ldt,
+                      const int8_t* k_codes, const int8_t* v_codes, const float* k_scale,
+                      const float* v_scale, int64_t pages, int kv_heads, int head_dim, int block,
+                      float scale, int window, int64_t max_new, int64_t max_len, void* out,
+                      int64_t ldo, float* lse, int32_t* status, void* workspace,
+                      size_t ws_bytes, void* stream) {
+  if ((dtype != PIQ_BF16 && dtype != PIQ_FP16) ||
+      !attn_sizes_ok(tokens, heads, kv_heads, head_dim, batch, max_new, max_len, window) ||
+      !kv8_cache_ok(k_codes, v_codes, k_scale, v_scale, pages, kv_heads, head_dim, block) ||
+      !kv8_table_ok(cu_q, lens, batch, block_table, table_width, ldt, status) ||
+      !(scale == scale) || scale - scale != 0.0f)
+    return PIQ_ERR_INVALID_ARG;
+  const int64_t row = static_cast<int64_t>(heads) * head_dim;
+  if (ldq < row || ldo < row || ldq % 8 != 0 || ldo % 8 != 0) return PIQ_ERR_INVALID_ARG;
+  if (tokens == 0 || max_new == 0) return PIQ_OK;
+  if (q == nullptr || out == nullptr || !ptr_aligned(q, 16) || !ptr_aligned(out, 16) ||
+      !ptr_aligned(lse, 4) || workspace == nullptr || !ptr_aligned(workspace, 256))
+    return PIQ_ERR_INVALID_ARG;
+  const AttnPlan a = plan_attention(tokens, heads, kv_heads, batch, max_new, max_len, window);
+  const AttnWs w = attn_ws(a, tokens, heads, head_dim);
+  if (ws_bytes < w.bytes) return PIQ_ERR_WORKSPACE_TOO_SMALL;
+  int rc = injected_fault();
+  DeviceInfo info;
+  if (rc == PIQ_OK) rc = device_info(&info);
+  if (rc != PIQ_OK) return rc;
+  Kv8Attn p;
+  p.q = q;
+  p.tokens = tokens;
+  p.ldq = ldq;
+  p.cu = cu_q;
+  p.lens = lens;
+  p.table = block_table;
+  p.width = table_width;
+  p.ldt = ldt;
+  p.kc = k_codes;
+  p.vc = v_codes;
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.pages = pages;
+  p.batch = static_cast<int>(batch);
+  p.heads = heads;
+  p.kv_heads = kv_heads;
+  p.block = block;
+  p.group = heads / kv_heads;
+  p.scale2 = scale * 1.4426950408889634f;
+  p.window = window;
+  p.max_new = max_new;
+  p.max_len = max_len;
+  p.chunk = a.chunk;
+  p.chunks = a.chunks;
+  p.out = out;
+  p.ldo = ldo;
+  p.lse = lse;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + w.ml_at);
+  p.status = status;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dtype == PIQ_BF16)
+    return head_dim == 128 ? launch_attention<__nv_bfloat16, 128>(p, a, s)
+                           : launch_attention<__nv_bfloat16, 64>(p, a, s);
+  return head_dim == 128 ? launch_attention<__half, 128>(p, a, s)
+                         : launch_attention<__half, 64>(p, a, s);
+}
+
+}  // extern "C"

@@ -1,0 +1,144 @@
+// Shared pieces of the 8-bit serving entries (int8.cu, kv8.cu, kv8_attn.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+
+namespace piq {
+
+// Largest contraction whose int32 sum is exact for any codes: 128 * 128 * in < 2^31.
+constexpr int64_t kInt8MaxIn = 131064;
+
+inline bool ptr_aligned(const void* p, uintptr_t a) {
+  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+// The caller's status words {code, detail}: the first error stays.
+__device__ __forceinline__ void note_status(int32_t* status, int code, int detail) {
+  if (status == nullptr) return;
+  if (atomicCAS(status, PIQ_OK, code) == PIQ_OK) status[1] = detail;
+}
+
+// Eight consecutive values of one row, as they lie in memory and in fp32.
+template <typename T>
+struct Eight {
+  static constexpr int kVecs = sizeof(T) / 2;  // 16-byte vectors
+  uint4 v[kVecs];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) v[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void floats(float (&f)[8]) const;
+};
+template <>
+__device__ __forceinline__ void Eight<float>::floats(float (&f)[8]) const {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    f[4 * i] = __uint_as_float(v[i].x);
+    f[4 * i + 1] = __uint_as_float(v[i].y);
+    f[4 * i + 2] = __uint_as_float(v[i].z);
+    f[4 * i + 3] = __uint_as_float(v[i].w);
+  }
+}
+template <>
+__device__ __forceinline__ void Eight<__nv_bfloat16>::floats(float (&f)[8]) const {
+  const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+template <>
+__device__ __forceinline__ void Eight<__half>::floats(float (&f)[8]) const {
+  const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    f[2 * i] = p.x;
+    f[2 * i + 1] = p.y;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ T from_float(float x);
+template <>
+__device__ __forceinline__ float from_float<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+template <>
+__device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
+
+// Largest magnitude as a bit pattern: ordered like the values, and an infinity
+// or NaN is larger than every finite one.
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+__device__ __forceinline__ uint32_t amax_bits8(const float (&f)[8], uint32_t m) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, abs_bits(f[i]));
+  return m;
+}
+
+// scale = amax / 127 (0 below 2^-126, NaN for an infinity or NaN).
+__device__ __forceinline__ float scale_of(uint32_t amax_bits) {
+  if (amax_bits >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
+  const float s = __fdiv_rn(__uint_as_float(amax_bits), 127.0f);
+  return s < 1.17549435e-38f ? 0.0f : s;
+}
+// 0 for scales 0 and NaN, so that their codes are 0.
+__device__ __forceinline__ float inverse_of(float scale) {
+  return scale > 0.0f ? __frcp_rn(scale) : 0.0f;
+}
+
+// rint(x) for |x| < 2^22, in the low byte: adding 1.5 * 2^23 leaves the integer,
+// rounded to nearest even, in the low bits of the sum (two's complement).
+__device__ __forceinline__ uint32_t code_bits(float x, float inverse) {
+  const float q = fminf(fmaxf(__fmul_rn(x, inverse), -127.0f), 127.0f);
+  return __float_as_uint(__fadd_rn(q, 12582912.0f));
+}
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+// A non-finite x meets inverse 0 only: its product is NaN, and fmaxf drops the
+// NaN for -127, so the zero codes of such a set are made here.
+__device__ __forceinline__ uint2 codes8(const float (&f)[8], float inverse) {
+  if (inverse == 0.0f) return make_uint2(0u, 0u);
+  uint32_t c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = code_bits(f[i], inverse);
+  return make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]));
+}
+
+// The sequence that ragged row `row` belongs to: the last b with cu[b] <= row,
+// found by a whole warp, 32 starts a step; -1 when row < cu[0] or row >=
+// cu[batch].  cu need not be valid: every index read lies in [0, batch].
+__device__ __forceinline__ int find_sequence(const int32_t* cu, int batch, int64_t row, int lane) {
+  int lo = 0, hi = batch + 1;  // answers lie in lo - 1 + (0 .. hi - lo)
+  while (hi - lo > 0) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + step * lane + step - 1;  // the last of this lane's run
+    const int probe = min(at, hi - 1);
+    const bool le = __ldg(cu + probe) <= row;
+    const unsigned votes = __ballot_sync(0xffffffffu, le);
+    // runs are 0 .. 31; the first run whose last start is beyond `row` holds the border
+    const int run = __ffs(~votes) - 1;
+    if (run < 0) { lo = hi; break; }
+    const int nlo = min(lo + step * run, hi);
+    const int nhi = min(nlo + step - 1, hi);
+    lo = nlo;
+    hi = max(nhi, nlo);
+    if (step == 1) { hi = lo; }
+  }
+  const int b = lo - 1;
+  return (b < 0 || b >= batch) ? -1 : b;
+}
+
+}  // namespace piq
