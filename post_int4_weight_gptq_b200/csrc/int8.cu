@@ -3,6 +3,7 @@
 //
 //   Y[t, c] = (sum_k qx[t, k] qw[c, k]) sx[t] sw[c] + bias[c]
 //
+// Here the quantizer and the entry points; the product is int8_gemm.cu.
 // The sum is exact in int32 (in <= 131064), so the result does not depend on
 // the order or the split of the sum; the scales and the bias are applied in
 // fp32 and the value is rounded once to Y's type.
@@ -27,8 +28,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
   constexpr int BLOCK = TPR < 256 ? 256 : TPR;
   constexpr int RPB = BLOCK / TPR;
   __shared__ uint32_t red[BLOCK / 32];
+  pdl_wait();  // first: the product may then start on the weights once every CTA is here
   pdl_launch_dependents();
-  pdl_wait();
   const int tr = threadIdx.x % TPR;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / TPR;
   const bool live = row < rows;
@@ -129,63 +130,6 @@ int launch_quantize_rows(const void* X, int dtype, int64_t rows, int64_t cols, i
   }
 }
 
-// ------------------------------------------------------------------ product
-// One warp: one output channel, eight tokens; lanes stride over k in runs of 16.
-constexpr int kTok = 8;
-
-template <typename T>
-__global__ void __launch_bounds__(256)
-    int8_dot_kernel(const int8_t* __restrict__ qx, int64_t ldq, const float* __restrict__ sx,
-                    int64_t tokens, int64_t in, const int8_t* __restrict__ W, int64_t out,
-                    int64_t ldw, const float* __restrict__ sw, const float* __restrict__ bias,
-                    T* __restrict__ Y, int64_t ldy) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (c >= out) return;
-  const int8_t* w = W + c * ldw;
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.y) * kTok; t0 < tokens;
-       t0 += static_cast<int64_t>(gridDim.y) * kTok) {
-    int acc[kTok] = {};
-    for (int64_t k = 16 * lane; k < in; k += 512) {
-      uint4 a = __ldg(reinterpret_cast<const uint4*>(w + k));
-      if (k + 16 > in) a.z = a.w = 0;  // in is a multiple of 8
-#pragma unroll
-      for (int t = 0; t < kTok; ++t) {
-        const int64_t row = min(t0 + t, tokens - 1);
-        const uint4 b = *reinterpret_cast<const uint4*>(qx + row * ldq + k);
-        acc[t] = __dp4a(static_cast<int>(a.x), static_cast<int>(b.x), acc[t]);
-        acc[t] = __dp4a(static_cast<int>(a.y), static_cast<int>(b.y), acc[t]);
-        acc[t] = __dp4a(static_cast<int>(a.z), static_cast<int>(b.z), acc[t]);
-        acc[t] = __dp4a(static_cast<int>(a.w), static_cast<int>(b.w), acc[t]);
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < kTok; ++t) {
-      const int s = __reduce_add_sync(0xffffffffu, acc[t]);
-      if (lane == 0 && t0 + t < tokens) {
-        float y = static_cast<float>(s) * sx[t0 + t] * sw[c];
-        if (bias != nullptr) y += bias[c];
-        Y[(t0 + t) * ldy + c] = from_float<T>(y);
-      }
-    }
-  }
-}
-
-template <typename T>
-int launch_dot_t(const int8_t* qx, int64_t ldq, const float* sx, int64_t tokens, int64_t in,
-                 const int8_t* W, int64_t out, int64_t ldw, const float* sw, const float* bias,
-                 T* Y, int64_t ldy, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(ceil_div(out, 8)),
-                  static_cast<unsigned>(std::min<int64_t>(ceil_div(tokens, kTok), 65535)));
-  note_launch();
-  return launch_pdl(int8_dot_kernel<T>, grid, dim3(256), 0, stream, qx, ldq, sx, tokens, in, W,
-                    out, ldw, sw, bias, Y, ldy) == cudaSuccess
-             ? PIQ_OK
-             : PIQ_ERR_CUDA;
-}
-
 // Workspace: the codes of X (rows padded to 16 bytes) and its scales.
 struct LinearWs {
   int64_t ldq;
@@ -258,17 +202,8 @@ int piq_int8_linear(const void* X, int dtype, int64_t tokens, int64_t in, int64_
   float* sx = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.scale_at);
   rc = launch_quantize_rows(X, dtype, tokens, in, ldx, qx, w.ldq, sx, s);
   if (rc != PIQ_OK) return rc;
-  switch (dtype) {
-    case PIQ_BF16:
-      return launch_dot_t(qx, w.ldq, sx, tokens, in, W, out, ldw, w_scale, bias,
-                          static_cast<__nv_bfloat16*>(Y), ldy, s);
-    case PIQ_FP16:
-      return launch_dot_t(qx, w.ldq, sx, tokens, in, W, out, ldw, w_scale, bias,
-                          static_cast<__half*>(Y), ldy, s);
-    default:
-      return launch_dot_t(qx, w.ldq, sx, tokens, in, W, out, ldw, w_scale, bias,
-                          static_cast<float*>(Y), ldy, s);
-  }
+  return launch_int8_gemm(qx, w.ldq, sx, tokens, in, W, out, ldw, w_scale, bias, Y, dtype, ldy,
+                          status, s);
 }
 
 }  // extern "C"

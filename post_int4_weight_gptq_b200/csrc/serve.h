@@ -11,6 +11,18 @@ namespace piq {
 // Largest contraction whose int32 sum is exact for any codes: 128 * 128 * in < 2^31.
 constexpr int64_t kInt8MaxIn = 131064;
 
+// How one int8 product is cut into tiles (int8_gemm.cu).
+struct Int8Plan {
+  bool pair;   // tiles of 256 channels on two CTAs, else 128 on one
+  int nt;      // tokens of a tile
+  int slices;  // of k
+};
+Int8Plan plan_int8(int64_t tokens, int64_t out, int64_t in, int sms);
+// Y = (qx W^T) sx sw + bias; qx, W int8 with 16-byte aligned rows, sx 16-byte aligned.
+int launch_int8_gemm(const int8_t* qx, int64_t ldq, const float* sx, int64_t tokens, int64_t in,
+                     const int8_t* W, int64_t out, int64_t ldw, const float* sw, const float* bias,
+                     void* Y, int dtype, int64_t ldy, int32_t* status, cudaStream_t stream);
+
 inline bool ptr_aligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }

@@ -101,7 +101,7 @@ def test_int8_linear(tokens, inp, out, bias, dtype):
 
 
 @pytest.mark.parametrize("tokens,inp,out", [(1, 28672, 520), (40, 28672, 300), (300, 11008, 640),
-                                            (1030, 4104, 2050)])
+                                            (1030, 4104, 2050), (2100, 264, 2400)])
 def test_int8_linear_long(tokens, inp, out):
     rng = np.random.default_rng(inp)
     x, w, ws, b = linear_case(rng, tokens, inp, out, BF16, True)
