@@ -21,46 +21,14 @@
 // is lost.  The sum of p stays in fp32.
 #include <algorithm>
 
-#include "serve.h"
+#include "kv8_attn.cuh"
 
 namespace piq {
 
-struct Kv8Attn {
-  const void* q;
-  int64_t tokens, ldq;
-  const int32_t *cu, *lens;
-  const int32_t* table;
-  int64_t width, ldt;
-  const int8_t *kc, *vc;
-  const float *ks, *vs;
-  int64_t pages;
-  int batch, heads, kv_heads, block, group;  // group = heads / kv_heads
-  float scale2;                              // scale * log2(e)
-  int64_t window;                            // 0: none
-  int64_t max_new, max_len;
-  int64_t chunk;                             // keys a CTA, a multiple of 128
-  int chunks;                                // most chunks of a sequence
-  void* out;
-  int64_t ldo;
-  float* lse;
-  float* part_o;   // [chunks][tokens][heads][D] when chunks > 1
-  float2* part_ml; // [chunks][tokens][heads]: running maximum (log2), sum
-  int32_t* status;
-};
-
 namespace {
 
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLow = -3.0e38f;      // below every score: "no key yet"
-constexpr float kPScale = 128.0f;     // 2^7
-constexpr float kSlack = 8.0f;        // log2 by which a score may pass the maximum
 constexpr int kWarps = 8;
 constexpr int kMaxPages = 256;        // pages of a chunk (4096 keys, blocks of 16)
-
-// Keys that some query of the sequence sees: [first, len).
-__device__ __forceinline__ int64_t first_key(int64_t len, int64_t n, int64_t window) {
-  return window > 0 ? max(static_cast<int64_t>(0), len - n + 1 - window) : 0;
-}
 
 __device__ __forceinline__ void halves_of(uint32_t w, uint32_t& even, uint32_t& odd) {
   // bytes 0 and 2, bytes 1 and 3, each + 128 under 0x6400, minus 1152
@@ -86,46 +54,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-template <typename T>
-__device__ __forceinline__ float to_float(T x);
-template <>
-__device__ __forceinline__ float to_float<__half>(__half x) { return __half2float(x); }
-template <>
-__device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 x) {
-  return __bfloat162float(x);
-}
-
-// A row of q in fp16 and the factor that undoes its scaling.  bf16 rows are
-// scaled by the power of two that brings their largest magnitude into [1, 2).
-template <typename T>
-__device__ __forceinline__ float row_exponent(float amax, float& mul);
-template <>
-__device__ __forceinline__ float row_exponent<__half>(float amax, float& mul) {
-  mul = 1.0f;
-  return amax < __uint_as_float(0x7F800000u) ? 1.0f : __uint_as_float(0x7FC00000u);
-}
-template <>
-__device__ __forceinline__ float row_exponent<__nv_bfloat16>(float amax, float& mul) {
-  const uint32_t e = __float_as_uint(amax) >> 23;  // biased exponent
-  if (e == 255u || !(amax == amax)) {
-    mul = 0.0f;
-    return __uint_as_float(0x7FC00000u);
-  }
-  if (e < 2u || e > 252u) {  // mul and its inverse stay normal numbers
-    const bool big = e > 252u;
-    mul = big ? 0x1p-126f : 0x1p126f;
-    return big ? 0x1p126f : 0x1p-126f;
-  }
-  mul = __uint_as_float((254u - e) << 23);
-  return __uint_as_float(e << 23);
 }
 
 // NT groups of eight query rows of one kv head (rows are (token, head) pairs,
@@ -155,21 +83,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
   const int64_t n = q1 - q0;
   if (n == 0) return;
   T* out = static_cast<T*>(p.out);
-  if (q0 < 0 || n < 0 || q1 > p.tokens || n > p.max_new || len < n || len > p.max_len ||
-      len > p.width * p.block) {
-    // lengths that cannot be: the sequence's rows, as far as they exist, are NaN
-    if (blockIdx.x != 0 || part != 0) return;
-    if (threadIdx.x == 0) note_status(p.status, PIQ_ERR_INVALID_ARG, b);
-    const int64_t t0 = max(q0, static_cast<int64_t>(0)), t1 = min(q1, p.tokens);
-    const float nan = __uint_as_float(0x7FC00000u);
-    for (int64_t t = t0; t < t1; ++t) {
-      for (int i = threadIdx.x; i < p.heads * D; i += blockDim.x)
-        out[t * p.ldo + i] = from_float<T>(nan);
-      if (p.lse != nullptr)
-        for (int i = threadIdx.x; i < p.heads; i += blockDim.x) p.lse[t * p.heads + i] = nan;
-    }
-    return;
-  }
+  if (bad_lengths<T, D>(p, b, q0, q1, len, blockIdx.x == 0 && part == 0)) return;
   const int64_t rows = n * p.group;
   const int64_t row0 = static_cast<int64_t>(rg) * ROWS;
   if (row0 >= rows) return;
@@ -529,9 +443,11 @@ __global__ void __launch_bounds__(128) kv8_join_kernel(Kv8Attn p) {
 
 // Keys a chunk: enough CTAs for two waves of two a multiprocessor, but no
 // chunk so short that joining it costs more than it spreads.
-constexpr int64_t kMinChunk = 256, kMaxChunk = 4096;
+constexpr int64_t kMinChunk = 256, kMaxChunk = 4096, kMinPromptChunk = 512;
+constexpr int64_t kManyRows = 32;  // rows a kv head above which the tensor-memory kernel runs
 
 struct AttnPlan {
+  bool prompt;       // kv8_prompt.cu
   int nt;            // groups of eight rows a CTA
   int64_t row_groups, chunk;
   int chunks;
@@ -541,11 +457,22 @@ AttnPlan plan_attention(int64_t tokens, int heads, int kv_heads, int64_t batch, 
                         int64_t window) {
   AttnPlan a;
   const int64_t rows = std::min(max_new, tokens) * (heads / kv_heads);
+  a.prompt = rows > kManyRows;
   a.nt = rows <= 8 ? 1 : 2;
   a.row_groups = std::max<int64_t>(1, ceil_div(rows, 8 * a.nt));
   int64_t span = max_len;  // most keys in sight of a sequence, from a block's (at most 128) start
   if (window > 0) span = std::min(span, window + max_new + 128);
   span = std::max<int64_t>(span, 1);
+  if (a.prompt) {
+    // whole multiprocessors: split the keys only where the rows leave some idle
+    const int64_t ctas = std::min(tokens * (heads / kv_heads) / kPromptRows + batch,
+                                  ceil_div(rows, kPromptRows) * batch) *
+                         kv_heads;
+    const int64_t want = std::max<int64_t>(1, 148 / ctas);
+    a.chunk = std::max(ceil_div(ceil_div(span, want), 128) * 128, kMinPromptChunk);
+    a.chunks = static_cast<int>(ceil_div(span, a.chunk));
+    return a;
+  }
   const int64_t ctas = a.row_groups * kv_heads * batch;
   const int64_t want = std::max<int64_t>(1, 4 * 148 / ctas);
   a.chunk = ceil_div(ceil_div(span, want), 128) * 128;
@@ -574,19 +501,28 @@ AttnWs attn_ws(const AttnPlan& a, int64_t tokens, int heads, int head_dim) {
 }
 
 template <typename T, int D>
+int launch_join(const Kv8Attn& p, cudaStream_t stream) {
+  note_launch();
+  return launch_pdl(kv8_join_kernel<T, D>, dim3(static_cast<unsigned>(p.tokens), p.heads),
+                    dim3(128), 0, stream, p) == cudaSuccess
+             ? PIQ_OK
+             : PIQ_ERR_CUDA;
+}
+
+template <typename T, int D>
 int launch_attention(const Kv8Attn& p, const AttnPlan& a, cudaStream_t stream) {
+  if (a.prompt) {
+    const int rc = launch_prompt<T, D>(p, stream);
+    if (rc != PIQ_OK) return rc;
+    return a.chunks == 1 ? PIQ_OK : launch_join<T, D>(p, stream);
+  }
   void (*kern)(Kv8Attn) = a.nt == 1 ? kv8_chunk_kernel<T, D, 1> : kv8_chunk_kernel<T, D, 2>;
   const unsigned gx = static_cast<unsigned>(a.row_groups * p.kv_heads);
   note_launch();
   if (launch_pdl(kern, dim3(gx, a.chunks, p.batch), dim3(32 * kWarps), 0,
                  stream, p) != cudaSuccess)
     return PIQ_ERR_CUDA;
-  if (a.chunks == 1) return PIQ_OK;
-  note_launch();
-  return launch_pdl(kv8_join_kernel<T, D>, dim3(static_cast<unsigned>(p.tokens), p.heads),
-                    dim3(128), 0, stream, p) == cudaSuccess
-             ? PIQ_OK
-             : PIQ_ERR_CUDA;
+  return a.chunks == 1 ? PIQ_OK : launch_join<T, D>(p, stream);
 }
 
 }  // namespace

@@ -1,0 +1,109 @@
+// Shared by the two attention kernels over the 8-bit cache (kv8_attn.cu: few
+// rows, kv8_prompt.cu: many).
+#pragma once
+
+#include "serve.h"
+
+namespace piq {
+
+struct Kv8Attn {
+  const void* q;
+  int64_t tokens, ldq;
+  const int32_t *cu, *lens;
+  const int32_t* table;
+  int64_t width, ldt;
+  const int8_t *kc, *vc;
+  const float *ks, *vs;
+  int64_t pages;
+  int batch, heads, kv_heads, block, group;  // group = heads / kv_heads
+  float scale2;                              // scale * log2(e)
+  int64_t window;                            // 0: none
+  int64_t max_new, max_len;
+  int64_t chunk;                             // keys a CTA, a multiple of 128
+  int chunks;                                // most chunks of a sequence
+  void* out;
+  int64_t ldo;
+  float* lse;
+  float* part_o;   // [chunks][tokens][heads][D] when chunks > 1
+  float2* part_ml; // [chunks][tokens][heads]: running maximum (log2), sum
+  int32_t* status;
+};
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLow = -3.0e38f;      // below every score: "no key yet"
+constexpr float kPScale = 128.0f;     // 2^7
+constexpr float kSlack = 8.0f;        // log2 by which a score may pass the maximum
+
+// Keys that some query of the sequence sees: [first, len).
+__device__ __forceinline__ int64_t first_key(int64_t len, int64_t n, int64_t window) {
+  return window > 0 ? max(static_cast<int64_t>(0), len - n + 1 - window) : 0;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <typename T>
+__device__ __forceinline__ float to_float(T x);
+template <>
+__device__ __forceinline__ float to_float<__half>(__half x) { return __half2float(x); }
+template <>
+__device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 x) {
+  return __bfloat162float(x);
+}
+
+// A row of q in fp16 and the factor that undoes its scaling.  bf16 rows are
+// scaled by the power of two that brings their largest magnitude into [1, 2).
+template <typename T>
+__device__ __forceinline__ float row_exponent(float amax, float& mul);
+template <>
+__device__ __forceinline__ float row_exponent<__half>(float amax, float& mul) {
+  mul = 1.0f;
+  return amax < __uint_as_float(0x7F800000u) ? 1.0f : __uint_as_float(0x7FC00000u);
+}
+template <>
+__device__ __forceinline__ float row_exponent<__nv_bfloat16>(float amax, float& mul) {
+  const uint32_t e = __float_as_uint(amax) >> 23;  // biased exponent
+  if (e == 255u || !(amax == amax)) {
+    mul = 0.0f;
+    return __uint_as_float(0x7FC00000u);
+  }
+  if (e < 2u || e > 252u) {  // mul and its inverse stay normal numbers
+    const bool big = e > 252u;
+    mul = big ? 0x1p-126f : 0x1p126f;
+    return big ? 0x1p126f : 0x1p-126f;
+  }
+  mul = __uint_as_float((254u - e) << 23);
+  return __uint_as_float(e << 23);
+}
+
+// Whether sequence b's lengths cannot be; then status is set and its rows, as far
+// as they exist, are NaN (`writer`: this CTA does that).
+template <typename T, int D>
+__device__ __forceinline__ bool bad_lengths(const Kv8Attn& p, int b, int64_t q0, int64_t q1,
+                                            int64_t len, bool writer) {
+  const int64_t n = q1 - q0;
+  if (q0 >= 0 && n >= 0 && q1 <= p.tokens && n <= p.max_new && len >= n && len <= p.max_len &&
+      len <= p.width * p.block)
+    return false;
+  if (!writer) return true;
+  if (threadIdx.x == 0) note_status(p.status, PIQ_ERR_INVALID_ARG, b);
+  const int64_t t0 = max(q0, static_cast<int64_t>(0)), t1 = min(q1, p.tokens);
+  const float nan = __uint_as_float(0x7FC00000u);
+  for (int64_t t = t0; t < t1; ++t) {
+    for (int i = threadIdx.x; i < p.heads * D; i += blockDim.x)
+      static_cast<T*>(p.out)[t * p.ldo + i] = from_float<T>(nan);
+    if (p.lse != nullptr)
+      for (int i = threadIdx.x; i < p.heads; i += blockDim.x) p.lse[t * p.heads + i] = nan;
+  }
+  return true;
+}
+
+// kv8_prompt.cu: the chunk kernel for many rows a kv head.
+constexpr int kPromptRows = 256;  // query rows a CTA
+template <typename T, int D>
+int launch_prompt(const Kv8Attn& p, cudaStream_t stream);
+
+}  // namespace piq

@@ -1,0 +1,545 @@
+// Attention of many new tokens over the 8-bit paged cache on the tensor cores
+// (tcgen05 kind::f16, fp32 in TMEM).
+//
+// A CTA holds 256 query rows of one kv head, two tiles of 128 rows; rows are
+// (token, head) pairs, the heads of the group fastest, so that all heads of the
+// group share the keys.  Keys pass in tiles of 128:
+//
+//   S = Q K^T    (both fp16 in shared memory; a code is exact in fp16)
+//   P = 2^7 2^(x - m) v_scale / v_max,  x = S scale k_scale   (TMEM over S, fp16)
+//   O += P V     (P from TMEM, V's codes fp16 in shared memory)
+//
+// with the running maximum m moved, and O rescaled, only when a score passes it
+// by 2^8.  v_max is the largest value scale of the keys in sight, found first;
+// the sum of 2^(x - m) is fp32.  The codes are widened to fp16 as they come from
+// the pages (no second copy of the cache exists): bytes go through registers to
+// the swizzled tiles both products read.
+//
+// 13 warps: 0 - 3 and 4 - 7 the softmax of tile 0 and 1 (a row a thread),
+// 8 - 11 widen keys and values, 12 issues the MMAs.  The two tiles alternate: one
+// tile's softmax runs while the tensor cores work for the other.  The MMAs of a
+// CTA execute in the order they are issued, so the scores of the next keys may be
+// issued over the P that the product before them reads.  Every wait is bounded.
+#include <algorithm>
+#include <atomic>
+
+#include "kv8_attn.cuh"
+
+namespace piq {
+
+namespace {
+
+constexpr int KT = 128;      // keys a tile
+constexpr int kThreads = 13 * 32;
+constexpr int kGran = KT / 16;  // 16-key granules: never across a page
+
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int32_t* status,
+                                         int where) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      note_status(status, PIQ_ERR_TIMEOUT, where);
+      return false;
+    }
+  }
+}
+// The same for a whole warp, which goes on or gives up together.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int32_t* status,
+                                          int where) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, status, where));
+}
+
+// fp16 A and B, fp32 D; B optionally MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool b_mn) {
+  return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// D += A B^T with A in tensor memory.
+__device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Four codes to four halves, in order.
+__device__ __forceinline__ uint2 widen4(uint32_t w) {
+  const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+  w ^= 0x80808080u;
+  const uint32_t lo = __byte_perm(w, 0x64646464u, 0x4140), hi = __byte_perm(w, 0x64646464u, 0x4342);
+  const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), off);
+  const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&hi), off);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// Byte offset of 16-byte piece `piece` (dims 8 piece ..) of row `row` in a tile of
+// 128 rows: halves of 64 dimensions, 128-byte rows, 128-byte swizzle.
+__device__ __forceinline__ uint32_t tile_at(int row, int piece) {
+  return (piece >> 3) * (KT * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+}
+
+template <int D>
+struct Layout {
+  static constexpr int TILE = KT * D * 2;  // fp16 bytes of 128 rows
+  static constexpr int K_AT = 2 * TILE, V_AT = 4 * TILE, BAR_AT = 6 * TILE;
+  static constexpr int BYTES = BAR_AT + 1024 + 1024;
+};
+
+struct Shared {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2];
+  uint64_t sc_full[4];
+  float ks[4][kGran], vf[4][kGran];  // scales of a tile: a ring of four, so that a slot is
+                                     // rewritten only after both softmaxes have left it
+  int vmax;
+  uint32_t tmem;
+};
+static_assert(sizeof(Shared) <= 1024, "barrier area");
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
+  using L = Layout<D>;
+  constexpr int PIECES = KT * D / 16 / 128;     // 16-code loads a thread and tile
+  constexpr int PER_KEY = D / 16;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  Shared& sh = *reinterpret_cast<Shared*>(smem + L::BAR_AT);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  pdl_launch_dependents();
+  pdl_wait();
+  // ------------------------------------------------------------- which rows
+  // Items of 256 rows are numbered without the lengths: sequence b's start at
+  // floor(cu[b] group / 256) + b.  The last ones, which see most keys, go first.
+  const int kvh = blockIdx.x % p.kv_heads;
+  const int64_t item = (gridDim.x - 1 - blockIdx.x) / p.kv_heads;
+  const int part = blockIdx.y;
+  int b;
+  {
+    int lo = 0, hi = p.batch;
+    while (hi > lo) {
+      const int step = (hi - lo + 31) / 32;
+      const int probe = min(lo + step * lane + step - 1, hi - 1);
+      const int64_t start = static_cast<int64_t>(__ldg(p.cu + probe)) * p.group / kPromptRows + probe;
+      const unsigned votes = __ballot_sync(0xffffffffu, start <= item);
+      const int run = __ffs(~votes) - 1;
+      if (run < 0) {
+        lo = hi;
+        break;
+      }
+      const int nlo = min(lo + step * run, hi);
+      hi = min(nlo + step - 1, hi);
+      lo = nlo;
+    }
+    b = lo - 1;
+  }
+  if (b < 0) return;
+  const int64_t q0 = __ldg(p.cu + b), q1 = __ldg(p.cu + b + 1), len = __ldg(p.lens + b);
+  const int64_t n = q1 - q0;
+  const int64_t row0 = (item - (q0 * p.group / kPromptRows + b)) * kPromptRows;
+  if (n == 0) return;
+  if (bad_lengths<T, D>(p, b, q0, q1, len, row0 == 0 && part == 0 && kvh == 0)) return;
+  const int64_t rows = n * p.group;
+  if (row0 >= rows) return;
+  const int nq = rows - row0 > 128 ? 2 : 1;  // tiles with rows in them
+  // ------------------------------------------------------------- which keys
+  const int64_t origin = first_key(len, n, p.window) / p.block * p.block;
+  const int64_t c0 = origin + part * p.chunk;
+  if (c0 >= len) return;
+  const int64_t c1 = min(c0 + p.chunk, len);
+  const bool single = len - origin <= p.chunk;
+  const int64_t last = min(row0 + kPromptRows, rows) - 1;
+  const int64_t see_lo = p.window > 0 ? len - n + row0 / p.group + 1 - p.window : 0;
+  const int64_t see_hi = len - n + last / p.group + 1;
+  const int64_t k0 = max(c0, see_lo & ~static_cast<int64_t>(15));
+  const int64_t k1 = min(c1, see_hi);
+  const int nt = k1 > k0 ? static_cast<int>((k1 - k0 + KT - 1) / KT) : 0;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.k_full[i], 4);
+      mbar_init(&sh.v_full[i], 4);
+      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.v_empty[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.pv_done[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.sc_full[i], 1);
+    sh.vmax = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  // ----------------------------------------- the largest value scale, the queries
+  if (nt > 0) {
+    const int64_t b0 = k0 / p.block, b1 = (k1 - 1) / p.block;
+    float top = 0.0f;
+    for (int64_t i = b0 + threadIdx.x; i <= b1; i += kThreads) {
+      const int pg = __ldg(p.table + b * p.ldt + i);
+      if (pg >= 0 && pg < p.pages)
+        top = fmaxf(top, __ldg(p.vs + static_cast<int64_t>(pg) * p.kv_heads + kvh));
+    }
+    top = warp_max(top);
+    if (lane == 0) atomicMax(&sh.vmax, __float_as_int(top));
+  }
+  const int64_t row = row0 + threadIdx.x;  // of softmax threads
+  const bool live = threadIdx.x < 256 && row < rows;
+  float rs = 0.0f;
+  if (warp < 4 * nq) {
+    uint4 v[D / 8];
+    const int64_t t = q0 + (live ? row : 0) / p.group;
+    const int head = kvh * p.group + static_cast<int>((live ? row : 0) % p.group);
+    const uint4* src =
+        reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + t * p.ldq + head * D);
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) v[i] = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      Eight<T> e;
+      float f[8];
+      e.v[0] = v[i];
+      e.floats(f);
+      m = amax_bits8(f, m);
+    }
+    float mul;
+    const float undo = row_exponent<T>(__uint_as_float(m), mul);
+    if (!(undo == undo)) mul = 0.0f;
+    rs = undo * fabsf(p.scale2);
+    if (p.scale2 < 0.0f) mul = -mul;
+    uint8_t* tile = smem + (threadIdx.x >> 7) * L::TILE;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      Eight<T> e;
+      float f[8];
+      e.v[0] = v[i];
+      e.floats(f);
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // rows that hold an infinity or NaN are zeros under a NaN factor
+        const float x = mul != 0.0f ? f[2 * j] * mul : 0.0f, y = mul != 0.0f ? f[2 * j + 1] * mul : 0.0f;
+        const __half2 h = __floats2half2_rn(x, y);
+        w[j] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      *reinterpret_cast<uint4*>(tile + tile_at(threadIdx.x & 127, i)) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const float vmax = __int_as_float(sh.vmax);
+
+  if (warp == 12) {
+    // --------------------------------------------------------------- MMA issuer
+    if (lane == 0 && nt > 0) {
+      constexpr uint32_t id_s = idesc_f16(128, KT, false), id_o = idesc_f16(128, D, true);
+      const uint32_t qa = smem_u32(smem);
+      auto scores = [&](int t, int st) {
+        const uint32_t a = qa + t * L::TILE, k = qa + L::K_AT + st * L::TILE;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * (KT * 128) + (kk & 3) * 32;
+          umma_bf16(tmem + t * KT, smem_desc(a + off, 16, 1024, kLayoutSw128),
+                   smem_desc(k + off, 16, 1024, kLayoutSw128), id_s, kk != 0);
+        }
+        umma_commit(&sh.s_full[t]);
+      };
+      bool ok = wait_bar(&sh.k_full[0], 0, p.status, 71);
+      if (ok) {
+        tc_fence_after();
+        for (int t = 0; t < nq; ++t) scores(t, 0);
+        umma_commit(&sh.k_empty[0]);
+      }
+      for (int j = 0; j < nt && ok; ++j) {
+        const int st = j & 1;
+        if (!(ok = wait_bar(&sh.v_full[st], (j >> 1) & 1, p.status, 72))) break;
+        const bool more = j + 1 < nt;
+        if (more && !(ok = wait_bar(&sh.k_full[st ^ 1], ((j + 1) >> 1) & 1, p.status, 73))) break;
+        for (int t = 0; t < nq; ++t) {
+          if (!(ok = wait_bar(&sh.p_full[t], j & 1, p.status, 74))) break;
+          tc_fence_after();
+          const uint32_t v = qa + L::V_AT + st * L::TILE;
+#pragma unroll
+          for (int kk = 0; kk < KT / 16; ++kk)
+            umma_f16_ts(tmem + 2 * KT + t * D, tmem + t * KT + kk * 8,
+                        smem_desc(v + kk * 2048, KT * 128, 1024, kLayoutSw128), id_o,
+                        (j | kk) != 0);
+          umma_commit(&sh.pv_done[t]);
+          if (more) scores(t, st ^ 1);
+        }
+        if (!ok) break;
+        umma_commit(&sh.v_empty[st]);
+        if (more) umma_commit(&sh.k_empty[st ^ 1]);
+      }
+      // the last arrival is in before the barriers' memory goes
+      if (ok) wait_bar(&sh.v_empty[(nt - 1) & 1], ((nt - 1) >> 1) & 1, p.status, 81);
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------ widening keys and values
+    const int tid = threadIdx.x - 256;
+    uint4 kr[PIECES], vr[PIECES];
+    int page = 0;  // of granule `lane` (lanes 0 - 7) of the next tile to load
+    float gks = 0.0f, gvs = 0.0f;
+    auto look = [&](int j) {
+      const int64_t key = k0 + static_cast<int64_t>(j) * KT + 16 * (lane & 7);
+      page = 0;
+      gks = gvs = 0.0f;
+      if (j < nt && key < k1) {
+        const int pg = __ldg(p.table + b * p.ldt + key / p.block);
+        gks = gvs = __uint_as_float(0x7FC00000u);
+        if (pg >= 0 && pg < p.pages) {
+          page = pg;
+          gks = __ldg(p.ks + static_cast<int64_t>(pg) * p.kv_heads + kvh);
+          gvs = __ldg(p.vs + static_cast<int64_t>(pg) * p.kv_heads + kvh);
+        } else {
+          note_status(p.status, PIQ_ERR_INVALID_ARG, b);
+        }
+      }
+    };
+    auto load = [&](const int8_t* codes, uint4 (&reg)[PIECES], int j) {
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        const int piece = i * 128 + tid, key = piece / PER_KEY;
+        const int pg = __shfl_sync(0xffffffffu, page, key >> 4);
+        const int off = static_cast<int>(k0 + static_cast<int64_t>(j) * KT + key) & (p.block - 1);
+        reg[i] = __ldg(reinterpret_cast<const uint4*>(
+            codes + ((static_cast<int64_t>(pg) * p.kv_heads + kvh) * p.block + off) * D + (piece % PER_KEY) * 16));
+      }
+    };
+    auto store = [&](uint8_t* tile, const uint4 (&reg)[PIECES]) {
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        const int piece = i * 128 + tid, key = piece / PER_KEY, c = piece % PER_KEY;
+        const uint2 a = widen4(reg[i].x), bb = widen4(reg[i].y), cc = widen4(reg[i].z),
+                    d = widen4(reg[i].w);
+        const uint4 lo = make_uint4(a.x, a.y, bb.x, bb.y), hi = make_uint4(cc.x, cc.y, d.x, d.y);
+        // pieces four apart share banks: one of them starts with its second half
+        const bool swap = (c & 4) != 0;
+        *reinterpret_cast<uint4*>(tile + tile_at(key, 2 * c + swap)) = swap ? hi : lo;
+        *reinterpret_cast<uint4*>(tile + tile_at(key, 2 * c + !swap)) = swap ? lo : hi;
+      }
+    };
+    look(0);
+    if (nt > 0) {
+      load(p.kc, kr, 0);
+      load(p.vc, vr, 0);
+    }
+    for (int j = 0; j < nt; ++j) {
+      const int st = j & 1, slot = j & 3;
+      const float tks = gks, tvs = gvs;
+      look(j + 1);
+      if (!wait_warp(&sh.k_empty[st], ((j >> 1) & 1) ^ 1u, p.status, 75)) break;
+      if (warp == 8) {
+        if (lane < kGran) {
+          sh.ks[slot][lane] = tks;
+          sh.vf[slot][lane] = vmax > 0.0f ? kPScale * (tvs / vmax) : (tvs == tvs ? 0.0f : tvs);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.sc_full[slot]);
+      }
+      store(smem + L::K_AT + st * L::TILE, kr);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.k_full[st]);
+      if (j + 1 < nt) load(p.kc, kr, j + 1);
+      if (!wait_warp(&sh.v_empty[st], ((j >> 1) & 1) ^ 1u, p.status, 76)) break;
+      store(smem + L::V_AT + st * L::TILE, vr);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.v_full[st]);
+      if (j + 1 < nt) load(p.vc, vr, j + 1);
+    }
+  } else if (warp < 4 * nq) {
+    // ------------------------------------------------------------------ softmax
+    const int t = warp >> 2;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + t * KT, to = tmem + lanes + 2 * KT + t * D;
+    const int64_t hi = live ? len - n + row / p.group + 1 : 0;
+    const int64_t lo = p.window > 0 ? hi - p.window : 0;
+    const float ninf = __uint_as_float(0xFF800000u);
+    float m = kLow, l = 0.0f;
+    bool ok = true;
+    for (int j = 0; j < nt; ++j) {
+      const int slot = j & 3;
+      const int64_t key0 = k0 + static_cast<int64_t>(j) * KT;
+      if (!(ok = wait_warp(&sh.sc_full[slot], (j >> 2) & 1, p.status, 77))) break;
+      if (!(ok = wait_warp(&sh.s_full[t], j & 1, p.status, 78))) break;
+      tc_fence_after();
+      // keys [from, to) of the tile are seen
+      const int from = static_cast<int>(max(lo - key0, static_cast<int64_t>(0)));
+      const int upto = static_cast<int>(min(max(hi - key0, static_cast<int64_t>(0)),
+                                            static_cast<int64_t>(KT)));
+      const bool mask = __any_sync(0xffffffffu, from > 0 || upto < KT);
+      float top = ninf;
+#pragma unroll
+      for (int c = 0; c < KT / 32; ++c) {
+        float s[32];
+        tmem_ld_32x32b_x32(ts + 32 * c, s);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          float x = ninf;
+          if (mask) {
+#pragma unroll
+            for (int i = 16 * g; i < 16 * g + 16; ++i)
+              x = fmaxf(x, 32 * c + i >= from && 32 * c + i < upto ? s[i] : ninf);
+          } else {
+#pragma unroll
+            for (int i = 16 * g; i < 16 * g + 16; ++i) x = fmaxf(x, s[i]);
+          }
+          top = fmaxf(top, x * (rs * sh.ks[slot][2 * c + g]));
+        }
+      }
+      if (__any_sync(0xffffffffu, top > m + kSlack)) {
+        const float nm = fmaxf(m, top);
+        const float f = exp2_fast(m - nm);
+        m = nm;
+        l *= f;
+        if (j > 0) {
+          if (!(ok = wait_warp(&sh.pv_done[t], (j - 1) & 1, p.status, 79))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            float o[16];
+            uint32_t w[16];
+            tmem_ld_32x32b_x16(to + 16 * c, o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * f);
+            tmem_st_x16(to + 16 * c, w);
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < KT / 32; ++c) {
+        float s[32];
+        uint32_t w[16];
+        tmem_ld_32x32b_x32(ts + 32 * c, s);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const float f = rs * sh.ks[slot][2 * c + g], vf = sh.vf[slot][2 * c + g];
+#pragma unroll
+          for (int i = 16 * g; i < 16 * g + 16; i += 2) {
+            float x0 = fmaf(s[i], f, -m), x1 = fmaf(s[i + 1], f, -m);
+            float f0 = vf, f1 = vf;
+            if (mask) {
+              const bool see0 = 32 * c + i >= from && 32 * c + i < upto;
+              const bool see1 = 32 * c + i + 1 >= from && 32 * c + i + 1 < upto;
+              x0 = see0 ? x0 : ninf;
+              x1 = see1 ? x1 : ninf;
+              f0 = see0 ? vf : 0.0f;
+              f1 = see1 ? vf : 0.0f;
+            }
+            const float e0 = exp2_fast(x0), e1 = exp2_fast(x1);
+            l += e0 + e1;
+            const __half2 h = __floats2half2_rn(e0 * f0, e1 * f1);
+            w[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        }
+        tmem_st_x16(ts + 16 * c, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.p_full[t]);
+    }
+    // ------------------------------------------------------------------- result
+    if (ok && nt > 0) ok = wait_warp(&sh.pv_done[t], (nt - 1) & 1, p.status, 80);
+    tc_fence_after();
+    const float norm = (single ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f) * (vmax / kPScale);
+    const int64_t tok = q0 + (live ? row : 0) / p.group;
+    const int head = kvh * p.group + static_cast<int>((live ? row : 0) % p.group);
+    const int64_t slot = (static_cast<int64_t>(part) * p.tokens + tok) * p.heads + head;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      float o[16];
+      __syncwarp();
+      if (nt > 0) {
+        tmem_ld_32x32b_x16(to + 16 * c, o);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = 0.0f;
+      }
+      if (live && single) {
+        T* at = static_cast<T*>(p.out) + tok * p.ldo + head * D + 16 * c;
+        uint4 v[2];
+        T* w = reinterpret_cast<T*>(v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = from_float<T>(o[i] * norm);
+        reinterpret_cast<uint4*>(at)[0] = v[0];
+        reinterpret_cast<uint4*>(at)[1] = v[1];
+      } else if (live) {
+        float4* at = reinterpret_cast<float4*>(p.part_o + slot * D + 16 * c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          at[i] = make_float4(o[4 * i] * norm, o[4 * i + 1] * norm, o[4 * i + 2] * norm,
+                              o[4 * i + 3] * norm);
+      }
+    }
+    if (live) {
+      if (!single)
+        p.part_ml[slot] = make_float2(m, l);
+      else if (p.lse != nullptr)
+        p.lse[tok * p.heads + head] =
+            l == 0.0f ? __uint_as_float(0xFF800000u) : (m + log2f(l)) * kLn2;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace
+
+template <typename T, int D>
+int launch_prompt(const Kv8Attn& p, cudaStream_t stream) {
+  static std::atomic<bool> set[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PIQ_ERR_CUDA;
+  if (dev >= 64 || !set[dev].load(std::memory_order_acquire)) {
+    const int rc = cuda_rc(cudaFuncSetAttribute(
+        kv8_prompt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::BYTES));
+    if (rc != PIQ_OK) return rc;
+    if (dev < 64) set[dev].store(true, std::memory_order_release);
+  }
+  const int64_t items = p.tokens * p.group / kPromptRows + p.batch;
+  note_launch();
+  return launch_pdl(kv8_prompt_kernel<T, D>,
+                    dim3(static_cast<unsigned>(items * p.kv_heads), p.chunks), dim3(kThreads),
+                    static_cast<size_t>(Layout<D>::BYTES), stream, p) == cudaSuccess
+             ? PIQ_OK
+             : PIQ_ERR_CUDA;
+}
+
+template int launch_prompt<__nv_bfloat16, 64>(const Kv8Attn&, cudaStream_t);
+template int launch_prompt<__nv_bfloat16, 128>(const Kv8Attn&, cudaStream_t);
+template int launch_prompt<__half, 64>(const Kv8Attn&, cudaStream_t);
+template int launch_prompt<__half, 128>(const Kv8Attn&, cudaStream_t);
+
+}  // namespace piq
