@@ -89,6 +89,37 @@ __device__ __forceinline__ uint2 widen4(uint32_t w) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
+// Two floats in one register pair.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// Which of a tile's keys 32 c .. 32 c + 31 lie in [from, upto).
+__device__ __forceinline__ uint32_t seen(int from, int upto, int c) {
+  const int a = min(max(from - 32 * c, 0), 32), b = min(max(upto - 32 * c, 0), 32);
+  const uint32_t below = b == 32 ? 0xFFFFFFFFu : (1u << b) - 1u;
+  return a == 32 ? 0u : below & ~((1u << a) - 1u);
+}
+
 // Byte offset of 16-byte piece `piece` (dims 8 piece ..) of row `row` in a tile of
 // 128 rows: halves of 64 dimensions, 128-byte rows, 128-byte swizzle.
 __device__ __forceinline__ uint32_t tile_at(int row, int piece) {
@@ -303,22 +334,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
     // ------------------------------------------------ widening keys and values
     const int tid = threadIdx.x - 256;
     uint4 kr[PIECES], vr[PIECES];
-    int page = 0;  // of granule `lane` (lanes 0 - 7) of the next tile to load
+    // Granule `lane & 7` of a tile: its table entry is fetched two tiles ahead, its
+    // scales one, so that neither is waited for.
+    int entry = 0, page = 0;
     float gks = 0.0f, gvs = 0.0f;
-    auto look = [&](int j) {
+    auto fetch = [&](int j) {
       const int64_t key = k0 + static_cast<int64_t>(j) * KT + 16 * (lane & 7);
+      entry = key < k1 ? __ldg(p.table + b * p.ldt + key / p.block) : -2;  // -2: no such keys
+    };
+    auto look = [&]() {
       page = 0;
-      gks = gvs = 0.0f;
-      if (j < nt && key < k1) {
-        const int pg = __ldg(p.table + b * p.ldt + key / p.block);
-        gks = gvs = __uint_as_float(0x7FC00000u);
-        if (pg >= 0 && pg < p.pages) {
-          page = pg;
-          gks = __ldg(p.ks + static_cast<int64_t>(pg) * p.kv_heads + kvh);
-          gvs = __ldg(p.vs + static_cast<int64_t>(pg) * p.kv_heads + kvh);
-        } else {
-          note_status(p.status, PIQ_ERR_INVALID_ARG, b);
-        }
+      gks = gvs = entry == -2 ? 0.0f : __uint_as_float(0x7FC00000u);
+      if (entry >= 0 && entry < p.pages) {
+        page = entry;
+        gks = __ldg(p.ks + static_cast<int64_t>(page) * p.kv_heads + kvh);
+        gvs = __ldg(p.vs + static_cast<int64_t>(page) * p.kv_heads + kvh);
+      } else if (entry != -2) {
+        note_status(p.status, PIQ_ERR_INVALID_ARG, b);
       }
     };
     auto load = [&](const int8_t* codes, uint4 (&reg)[PIECES], int j) {
@@ -344,7 +376,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
         *reinterpret_cast<uint4*>(tile + tile_at(key, 2 * c + !swap)) = swap ? lo : hi;
       }
     };
-    look(0);
+    fetch(0);
+    look();
+    fetch(1);
     if (nt > 0) {
       load(p.kc, kr, 0);
       load(p.vc, vr, 0);
@@ -352,7 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
     for (int j = 0; j < nt; ++j) {
       const int st = j & 1, slot = j & 3;
       const float tks = gks, tvs = gvs;
-      look(j + 1);
+      look();        // of tile j + 1
+      fetch(j + 2);
       if (!wait_warp(&sh.k_empty[st], ((j >> 1) & 1) ^ 1u, p.status, 75)) break;
       if (warp == 8) {
         if (lane < kGran) {
@@ -382,7 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
     const int64_t hi = live ? len - n + row / p.group + 1 : 0;
     const int64_t lo = p.window > 0 ? hi - p.window : 0;
     const float ninf = __uint_as_float(0xFF800000u);
-    float m = kLow, l = 0.0f;
+    float m = kLow;
+    uint64_t l2 = 0;  // the sum, even and odd keys
     bool ok = true;
     for (int j = 0; j < nt; ++j) {
       const int slot = j & 3;
@@ -396,21 +432,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
                                             static_cast<int64_t>(KT)));
       const bool mask = __any_sync(0xffffffffu, from > 0 || upto < KT);
       float top = ninf;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < KT / 32; ++c) {
         float s[32];
         tmem_ld_32x32b_x32(ts + 32 * c, s);
+        if (mask) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[i] = ((seen(from, upto, c) >> i) & 1u) ? s[i] : ninf;
+        }
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          float x = ninf;
-          if (mask) {
+          float x = s[16 * g];
 #pragma unroll
-            for (int i = 16 * g; i < 16 * g + 16; ++i)
-              x = fmaxf(x, 32 * c + i >= from && 32 * c + i < upto ? s[i] : ninf);
-          } else {
-#pragma unroll
-            for (int i = 16 * g; i < 16 * g + 16; ++i) x = fmaxf(x, s[i]);
-          }
+          for (int i = 1; i < 16; ++i) x = fmaxf(x, s[16 * g + i]);
           top = fmaxf(top, x * (rs * sh.ks[slot][2 * c + g]));
         }
       }
@@ -418,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
         const float nm = fmaxf(m, top);
         const float f = exp2_fast(m - nm);
         m = nm;
-        l *= f;
+        l2 = mul2(l2, pack2(f, f));
         if (j > 0) {
           if (!(ok = wait_warp(&sh.pv_done[t], (j - 1) & 1, p.status, 79))) break;
           tc_fence_after();
@@ -433,29 +467,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
           }
         }
       }
-#pragma unroll
+      const uint64_t nm2 = pack2(-m, -m);
+#pragma unroll 1
       for (int c = 0; c < KT / 32; ++c) {
         float s[32];
         uint32_t w[16];
         tmem_ld_32x32b_x32(ts + 32 * c, s);
+        const uint32_t bits = mask ? seen(from, upto, c) : 0xFFFFFFFFu;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           const float f = rs * sh.ks[slot][2 * c + g], vf = sh.vf[slot][2 * c + g];
+          const uint64_t f2 = pack2(f, f), vf2 = pack2(vf, vf);
 #pragma unroll
           for (int i = 16 * g; i < 16 * g + 16; i += 2) {
-            float x0 = fmaf(s[i], f, -m), x1 = fmaf(s[i + 1], f, -m);
-            float f0 = vf, f1 = vf;
+            float x0, x1, y0, y1;
+            unpack2(fma2(pack2(s[i], s[i + 1]), f2, nm2), x0, x1);
             if (mask) {
-              const bool see0 = 32 * c + i >= from && 32 * c + i < upto;
-              const bool see1 = 32 * c + i + 1 >= from && 32 * c + i + 1 < upto;
-              x0 = see0 ? x0 : ninf;
-              x1 = see1 ? x1 : ninf;
-              f0 = see0 ? vf : 0.0f;
-              f1 = see1 ? vf : 0.0f;
+              x0 = (bits >> i) & 1u ? x0 : ninf;
+              x1 = (bits >> (i + 1)) & 1u ? x1 : ninf;
             }
-            const float e0 = exp2_fast(x0), e1 = exp2_fast(x1);
-            l += e0 + e1;
-            const __half2 h = __floats2half2_rn(e0 * f0, e1 * f1);
+            const uint64_t e = pack2(exp2_fast(x0), exp2_fast(x1));
+            l2 = add2(l2, e);
+            unpack2(mul2(e, vf2), y0, y1);
+            if (mask) {  // 0 times the scale of a block that holds a NaN is not 0
+              y0 = (bits >> i) & 1u ? y0 : 0.0f;
+              y1 = (bits >> (i + 1)) & 1u ? y1 : 0.0f;
+            }
+            const __half2 h = __floats2half2_rn(y0, y1);
             w[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
           }
         }
@@ -469,6 +507,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
     // ------------------------------------------------------------------- result
     if (ok && nt > 0) ok = wait_warp(&sh.pv_done[t], (nt - 1) & 1, p.status, 80);
     tc_fence_after();
+    float la, lb;
+    unpack2(l2, la, lb);
+    const float l = la + lb;
     const float norm = (single ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f) * (vmax / kPScale);
     const int64_t tok = q0 + (live ? row : 0) / p.group;
     const int head = kvh * p.group + static_cast<int>((live ? row : 0) % p.group);
