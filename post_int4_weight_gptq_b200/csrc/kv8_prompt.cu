@@ -15,8 +15,9 @@
 // the pages (no second copy of the cache exists): bytes go through registers to
 // the swizzled tiles both products read.
 //
-// 13 warps: 0 - 3 and 4 - 7 the softmax of tile 0 and 1 (a row a thread),
-// 8 - 11 widen keys and values, 12 issues the MMAs.  The two tiles alternate: one
+// 16 warps: 0 - 3 and 4 - 7 the softmax of tile 0 and 1 (a row a thread),
+// 8 - 11 widen keys and values, 12 issues the MMAs (13 - 15 only give their
+// registers away).  The two tiles alternate: one
 // tile's softmax runs while the tensor cores work for the other.  The MMAs of a
 // CTA execute in the order they are issued, so the scores of the next keys may be
 // issued over the P that the product before them reads.  Every wait is bounded.
@@ -30,7 +31,7 @@ namespace piq {
 namespace {
 
 constexpr int KT = 128;      // keys a tile
-constexpr int kThreads = 13 * 32;
+constexpr int kThreads = 16 * 32;
 constexpr int kGran = KT / 16;  // 16-key granules: never across a page
 
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int32_t* status,
@@ -77,6 +78,20 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// A warpgroup's registers a thread.  The block is launched with 16 warps of 128
+// registers; the shares below (2 x 136 softmax, 168 widening, 64 the rest) stay
+// within that.
+constexpr int kRegSoftmax = 136, kRegWiden = 168, kRegIssue = 64;
+static_assert(2 * kRegSoftmax + kRegWiden + kRegIssue <= 4 * 128, "more than the launch has");
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Four codes to four halves, in order.
@@ -147,7 +162,6 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
   using L = Layout<D>;
   constexpr int PIECES = KT * D / 16 / 128;     // 16-code loads a thread and tile
-  constexpr int PER_KEY = D / 16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -238,21 +252,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
   const bool live = threadIdx.x < 256 && row < rows;
   float rs = 0.0f;
   if (warp < 4 * nq) {
-    uint4 v[D / 8];
     const int64_t t = q0 + (live ? row : 0) / p.group;
     const int head = kvh * p.group + static_cast<int>((live ? row : 0) % p.group);
-    const uint4* src =
-        reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + t * p.ldq + head * D);
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) v[i] = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+    const T* src = static_cast<const T*>(p.q) + t * p.ldq + head * D;
+    // twice over the row: its largest magnitude, then (from the cache) its halves
     uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      Eight<T> e;
-      float f[8];
-      e.v[0] = v[i];
-      e.floats(f);
-      m = amax_bits8(f, m);
+    if (live) {
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        Eight<T> e;
+        float f[8];
+        e.load(src + 8 * i);
+        e.floats(f);
+        m = amax_bits8(f, m);
+      }
     }
     float mul;
     const float undo = row_exponent<T>(__uint_as_float(m), mul);
@@ -260,11 +273,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
     rs = undo * fabsf(p.scale2);
     if (p.scale2 < 0.0f) mul = -mul;
     uint8_t* tile = smem + (threadIdx.x >> 7) * L::TILE;
-#pragma unroll
+#pragma unroll 4
     for (int i = 0; i < D / 8; ++i) {
       Eight<T> e;
       float f[8];
-      e.v[0] = v[i];
+      if (live)
+        e.load(src + 8 * i);
+      else
+        e.zero();
       e.floats(f);
       uint32_t w[4];
 #pragma unroll
@@ -285,9 +301,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
   const uint32_t tmem = sh.tmem;
   const float vmax = __int_as_float(sh.vmax);
 
-  if (warp == 12) {
+  if (warp >= 12) {
     // --------------------------------------------------------------- MMA issuer
-    if (lane == 0 && nt > 0) {
+    fewer_registers<kRegIssue>();
+    if (warp == 12 && lane == 0 && nt > 0) {
       constexpr uint32_t id_s = idesc_f16(128, KT, false), id_o = idesc_f16(128, D, true);
       const uint32_t qa = smem_u32(smem);
       auto scores = [&](int t, int st) {
@@ -332,18 +349,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
     }
   } else if (warp >= 8) {
     // ------------------------------------------------ widening keys and values
+    more_registers<kRegWiden>();
+    // A granule of 16 keys is one run of 16 D bytes; the 128 threads take 128 / D
+    // of them at a time, 16 bytes each.  Four lanes share a key's 64 dimensions and
+    // the next four the key after it, whose swizzle puts their halves into the other
+    // banks.
+    constexpr int GPL = 128 / D;                       // granules a load
     const int tid = threadIdx.x - 256;
+    const int piece = tid & 3, key = ((tid >> 2) & 1) + 2 * ((tid >> 3) & 7);
+    const int gsel = D == 128 ? 0 : tid >> 6, half = D == 128 ? tid >> 6 : 0;
+    const int from = key * D + half * 64 + piece * 16;  // in the granule
+    const uint32_t to0 = tile_at(gsel * 16 + key, half * 8 + 2 * piece),
+                   to1 = tile_at(gsel * 16 + key, half * 8 + 2 * piece + 1);
     uint4 kr[PIECES], vr[PIECES];
     // Granule `lane & 7` of a tile: its table entry is fetched two tiles ahead, its
     // scales one, so that neither is waited for.
-    int entry = 0, page = 0;
+    int entry = 0;
+    int64_t base = 0;
     float gks = 0.0f, gvs = 0.0f;
+    const int shift = __ffs(p.block) - 1;
+    const int32_t* table = p.table + b * p.ldt;
     auto fetch = [&](int j) {
-      const int64_t key = k0 + static_cast<int64_t>(j) * KT + 16 * (lane & 7);
-      entry = key < k1 ? __ldg(p.table + b * p.ldt + key / p.block) : -2;  // -2: no such keys
+      const int64_t k = k0 + static_cast<int64_t>(j) * KT + 16 * (lane & 7);
+      entry = k < k1 ? __ldg(table + (k >> shift)) : -2;  // -2: no such keys
     };
-    auto look = [&]() {
-      page = 0;
+    auto look = [&](int j) {
+      int page = 0;
       gks = gvs = entry == -2 ? 0.0f : __uint_as_float(0x7FC00000u);
       if (entry >= 0 && entry < p.pages) {
         page = entry;
@@ -352,41 +383,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
       } else if (entry != -2) {
         note_status(p.status, PIQ_ERR_INVALID_ARG, b);
       }
+      const int off = static_cast<int>(k0 + static_cast<int64_t>(j) * KT + 16 * (lane & 7)) &
+                      (p.block - 1);
+      base = ((static_cast<int64_t>(page) * p.kv_heads + kvh) * p.block + off) * D;
     };
-    auto load = [&](const int8_t* codes, uint4 (&reg)[PIECES], int j) {
+    auto load = [&](const int8_t* codes, uint4 (&reg)[PIECES]) {
 #pragma unroll
-      for (int i = 0; i < PIECES; ++i) {
-        const int piece = i * 128 + tid, key = piece / PER_KEY;
-        const int pg = __shfl_sync(0xffffffffu, page, key >> 4);
-        const int off = static_cast<int>(k0 + static_cast<int64_t>(j) * KT + key) & (p.block - 1);
+      for (int i = 0; i < PIECES; ++i)
         reg[i] = __ldg(reinterpret_cast<const uint4*>(
-            codes + ((static_cast<int64_t>(pg) * p.kv_heads + kvh) * p.block + off) * D + (piece % PER_KEY) * 16));
-      }
+            codes + __shfl_sync(0xffffffffu, base, i * GPL + gsel) + from));
     };
     auto store = [&](uint8_t* tile, const uint4 (&reg)[PIECES]) {
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
-        const int piece = i * 128 + tid, key = piece / PER_KEY, c = piece % PER_KEY;
-        const uint2 a = widen4(reg[i].x), bb = widen4(reg[i].y), cc = widen4(reg[i].z),
-                    d = widen4(reg[i].w);
-        const uint4 lo = make_uint4(a.x, a.y, bb.x, bb.y), hi = make_uint4(cc.x, cc.y, d.x, d.y);
-        // pieces four apart share banks: one of them starts with its second half
-        const bool swap = (c & 4) != 0;
-        *reinterpret_cast<uint4*>(tile + tile_at(key, 2 * c + swap)) = swap ? hi : lo;
-        *reinterpret_cast<uint4*>(tile + tile_at(key, 2 * c + !swap)) = swap ? lo : hi;
+        const uint2 x = widen4(reg[i].x), y = widen4(reg[i].y), z = widen4(reg[i].z),
+                    w = widen4(reg[i].w);
+        *reinterpret_cast<uint4*>(tile + to0 + i * GPL * 2048) = make_uint4(x.x, x.y, y.x, y.y);
+        *reinterpret_cast<uint4*>(tile + to1 + i * GPL * 2048) = make_uint4(z.x, z.y, w.x, w.y);
       }
     };
     fetch(0);
-    look();
+    look(0);
     fetch(1);
     if (nt > 0) {
-      load(p.kc, kr, 0);
-      load(p.vc, vr, 0);
+      load(p.kc, kr);
+      load(p.vc, vr);
     }
     for (int j = 0; j < nt; ++j) {
       const int st = j & 1, slot = j & 3;
       const float tks = gks, tvs = gvs;
-      look();        // of tile j + 1
+      look(j + 1);
       fetch(j + 2);
       if (!wait_warp(&sh.k_empty[st], ((j >> 1) & 1) ^ 1u, p.status, 75)) break;
       if (warp == 8) {
@@ -401,16 +427,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.k_full[st]);
-      if (j + 1 < nt) load(p.kc, kr, j + 1);
+      if (j + 1 < nt) load(p.kc, kr);
       if (!wait_warp(&sh.v_empty[st], ((j >> 1) & 1) ^ 1u, p.status, 76)) break;
       store(smem + L::V_AT + st * L::TILE, vr);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.v_full[st]);
-      if (j + 1 < nt) load(p.vc, vr, j + 1);
+      if (j + 1 < nt) load(p.vc, vr);
     }
-  } else if (warp < 4 * nq) {
+  } else {
     // ------------------------------------------------------------------ softmax
+    more_registers<kRegSoftmax>();
+    if (warp < 4 * nq) {
     const int t = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + t * KT, to = tmem + lanes + 2 * KT + t * D;
@@ -546,6 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
       else if (p.lse != nullptr)
         p.lse[tok * p.heads + head] =
             l == 0.0f ? __uint_as_float(0xFF800000u) : (m + log2f(l)) * kLn2;
+    }
     }
   }
   tc_fence_before();
