@@ -135,10 +135,121 @@ __device__ __forceinline__ uint32_t seen(int from, int upto, int c) {
   return a == 32 ? 0u : below & ~((1u << a) - 1u);
 }
 
+// The largest of a row's 128 scores (scaled), this thread's TMEM lane at ts.
+// MASK: only keys [from, upto) count.  Kept apart from the unmasked form, which
+// all but a few tiles take: selects for every key cost as much as the rest.
+template <bool MASK>
+__device__ __forceinline__ float row_max(uint32_t ts, float rs, const float* ks, int from,
+                                         int upto) {
+  const float ninf = __uint_as_float(0xFF800000u);
+  float top = ninf;
+#pragma unroll 1
+  for (int c = 0; c < KT / 32; ++c) {
+    float s[32];
+    tmem_ld_32x32b_x32(ts + 32 * c, s);
+    if (MASK) {
+      const uint32_t bits = seen(from, upto, c);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s[i] = (bits >> i) & 1u ? s[i] : ninf;
+    }
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      // a score times the (positive) scales is monotone in it
+      float x = fmaxf(s[16 * g], s[16 * g + 1]), y = fmaxf(s[16 * g + 2], s[16 * g + 3]);
+#pragma unroll
+      for (int i = 4; i < 16; i += 4) {
+        x = fmaxf(fmaxf(x, s[16 * g + i]), s[16 * g + i + 1]);
+        y = fmaxf(fmaxf(y, s[16 * g + i + 2]), s[16 * g + i + 3]);
+      }
+      top = fmaxf(top, fmaxf(x, y) * (rs * ks[2 * c + g]));
+    }
+  }
+  return top;
+}
+
+// The row's probabilities relative to m, summed into l2, and times the blocks'
+// value factors as halves over the scores.
+template <bool MASK>
+__device__ __forceinline__ void row_weights(uint32_t ts, float rs, float m, const float* ks,
+                                            const float* vfs, int from, int upto, uint64_t& l2) {
+  const float ninf = __uint_as_float(0xFF800000u);
+  const uint64_t nm2 = pack2(-m, -m);
+#pragma unroll 1
+  for (int c = 0; c < KT / 32; ++c) {
+    float s[32];
+    uint32_t w[16];
+    tmem_ld_32x32b_x32(ts + 32 * c, s);
+    const uint32_t bits = MASK ? seen(from, upto, c) : 0xFFFFFFFFu;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const float f = rs * ks[2 * c + g], vf = vfs[2 * c + g];
+      const uint64_t f2 = pack2(f, f), vf2 = pack2(vf, vf);
+#pragma unroll
+      for (int i = 16 * g; i < 16 * g + 16; i += 2) {
+        float x0, x1, y0, y1;
+        unpack2(fma2(pack2(s[i], s[i + 1]), f2, nm2), x0, x1);
+        if (MASK) {
+          x0 = (bits >> i) & 1u ? x0 : ninf;
+          x1 = (bits >> (i + 1)) & 1u ? x1 : ninf;
+        }
+        const uint64_t e = pack2(exp2_fast(x0), exp2_fast(x1));
+        l2 = add2(l2, e);
+        unpack2(mul2(e, vf2), y0, y1);
+        if (MASK) {  // 0 times the scale of a block that holds a NaN is not 0
+          y0 = (bits >> i) & 1u ? y0 : 0.0f;
+          y1 = (bits >> (i + 1)) & 1u ? y1 : 0.0f;
+        }
+        const __half2 h = __floats2half2_rn(y0, y1);
+        w[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    tmem_st_x16(ts + 16 * c, w);
+  }
+}
+
 // Byte offset of 16-byte piece `piece` (dims 8 piece ..) of row `row` in a tile of
 // 128 rows: halves of 64 dimensions, 128-byte rows, 128-byte swizzle.
 __device__ __forceinline__ uint32_t tile_at(int row, int piece) {
   return (piece >> 3) * (KT * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+}
+
+// Row `row` of a query tile from src (zeros for nullptr), as halves; returns the
+// positive factor of its scores (log2 units), the sign of scale2 going into the
+// halves.  A row that holds an infinity or NaN is zeros under a NaN factor.
+template <typename T, int D>
+__device__ __forceinline__ float stage_query(const T* src, uint8_t* tile, int row, float scale2) {
+  Eight<T> v[D / 8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    if (src != nullptr)
+      v[i].load(src + 8 * i);
+    else
+      v[i].zero();
+  }
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    float f[8];
+    v[i].floats(f);
+    m = amax_bits8(f, m);
+  }
+  float mul;
+  const float undo = row_exponent<T>(__uint_as_float(m), mul);
+  const bool fine = undo == undo;
+  if (scale2 < 0.0f) mul = -mul;
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    float f[8];
+    uint32_t w[4];
+    v[i].floats(f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __half2 h = __floats2half2_rn(f[2 * j] * mul, f[2 * j + 1] * mul);
+      w[j] = fine ? *reinterpret_cast<const uint32_t*>(&h) : 0u;
+    }
+    *reinterpret_cast<uint4*>(tile + tile_at(row, i)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return undo * fabsf(scale2);
 }
 
 template <int D>
@@ -150,7 +261,7 @@ struct Layout {
 
 struct Shared {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2];
-  uint64_t sc_full[4];
+  uint64_t sc_full[4], q_full;
   float ks[4][kGran], vf[4][kGran];  // scales of a tile: a ring of four, so that a slot is
                                      // rewritten only after both softmaxes have left it
   int vmax;
@@ -228,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
       mbar_init(&sh.pv_done[i], 1);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&sh.sc_full[i], 1);
+    mbar_init(&sh.q_full, 4 * nq);
     sh.vmax = 0;
     fence_mbar_init();
   }
@@ -235,71 +347,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
+  tc_fence_before();
   __syncthreads();
-  // ----------------------------------------- the largest value scale, the queries
-  if (nt > 0) {
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  // the largest value scale, found by the widening warps
+  auto find_vmax = [&]() {
     const int64_t b0 = k0 / p.block, b1 = (k1 - 1) / p.block;
     float top = 0.0f;
-    for (int64_t i = b0 + threadIdx.x; i <= b1; i += kThreads) {
+    for (int64_t i = b0 + threadIdx.x - 256; i <= b1; i += 128) {
       const int pg = __ldg(p.table + b * p.ldt + i);
       if (pg >= 0 && pg < p.pages)
         top = fmaxf(top, __ldg(p.vs + static_cast<int64_t>(pg) * p.kv_heads + kvh));
     }
     top = warp_max(top);
     if (lane == 0) atomicMax(&sh.vmax, __float_as_int(top));
-  }
-  const int64_t row = row0 + threadIdx.x;  // of softmax threads
-  const bool live = threadIdx.x < 256 && row < rows;
-  float rs = 0.0f;
-  if (warp < 4 * nq) {
-    const int64_t t = q0 + (live ? row : 0) / p.group;
-    const int head = kvh * p.group + static_cast<int>((live ? row : 0) % p.group);
-    const T* src = static_cast<const T*>(p.q) + t * p.ldq + head * D;
-    // twice over the row: its largest magnitude, then (from the cache) its halves
-    uint32_t m = 0;
-    if (live) {
-#pragma unroll 4
-      for (int i = 0; i < D / 8; ++i) {
-        Eight<T> e;
-        float f[8];
-        e.load(src + 8 * i);
-        e.floats(f);
-        m = amax_bits8(f, m);
-      }
-    }
-    float mul;
-    const float undo = row_exponent<T>(__uint_as_float(m), mul);
-    if (!(undo == undo)) mul = 0.0f;
-    rs = undo * fabsf(p.scale2);
-    if (p.scale2 < 0.0f) mul = -mul;
-    uint8_t* tile = smem + (threadIdx.x >> 7) * L::TILE;
-#pragma unroll 4
-    for (int i = 0; i < D / 8; ++i) {
-      Eight<T> e;
-      float f[8];
-      if (live)
-        e.load(src + 8 * i);
-      else
-        e.zero();
-      e.floats(f);
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        // rows that hold an infinity or NaN are zeros under a NaN factor
-        const float x = mul != 0.0f ? f[2 * j] * mul : 0.0f, y = mul != 0.0f ? f[2 * j + 1] * mul : 0.0f;
-        const __half2 h = __floats2half2_rn(x, y);
-        w[j] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-      *reinterpret_cast<uint4*>(tile + tile_at(threadIdx.x & 127, i)) =
-          make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    fence_proxy_async_smem();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sh.tmem;
-  const float vmax = __int_as_float(sh.vmax);
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+  };
 
   if (warp >= 12) {
     // --------------------------------------------------------------- MMA issuer
@@ -317,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
         }
         umma_commit(&sh.s_full[t]);
       };
-      bool ok = wait_bar(&sh.k_full[0], 0, p.status, 71);
+      bool ok = wait_bar(&sh.q_full, 0, p.status, 70) && wait_bar(&sh.k_full[0], 0, p.status, 71);
       if (ok) {
         tc_fence_after();
         for (int t = 0; t < nq; ++t) scores(t, 0);
@@ -408,7 +472,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
     if (nt > 0) {
       load(p.kc, kr);
       load(p.vc, vr);
+      find_vmax();
     }
+    const float vmax = __int_as_float(sh.vmax);
     for (int j = 0; j < nt; ++j) {
       const int st = j & 1, slot = j & 3;
       const float tks = gks, tvs = gvs;
@@ -439,142 +505,107 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
     // ------------------------------------------------------------------ softmax
     more_registers<kRegSoftmax>();
     if (warp < 4 * nq) {
-    const int t = warp >> 2;
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + t * KT, to = tmem + lanes + 2 * KT + t * D;
-    const int64_t hi = live ? len - n + row / p.group + 1 : 0;
-    const int64_t lo = p.window > 0 ? hi - p.window : 0;
-    const float ninf = __uint_as_float(0xFF800000u);
-    float m = kLow;
-    uint64_t l2 = 0;  // the sum, even and odd keys
-    bool ok = true;
-    for (int j = 0; j < nt; ++j) {
-      const int slot = j & 3;
-      const int64_t key0 = k0 + static_cast<int64_t>(j) * KT;
-      if (!(ok = wait_warp(&sh.sc_full[slot], (j >> 2) & 1, p.status, 77))) break;
-      if (!(ok = wait_warp(&sh.s_full[t], j & 1, p.status, 78))) break;
+      const int64_t row = row0 + threadIdx.x;
+      const bool live = row < rows;
+      const int64_t tok = q0 + (live ? row : 0) / p.group;
+      const int head = kvh * p.group + static_cast<int>((live ? row : 0) % p.group);
+      const float rs = stage_query<T, D>(
+          live ? static_cast<const T*>(p.q) + tok * p.ldq + head * D : nullptr,
+          smem + (threadIdx.x >> 7) * L::TILE, threadIdx.x & 127, p.scale2);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_full);
+      const int t = warp >> 2;
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t ts = tmem + lanes + t * KT, to = tmem + lanes + 2 * KT + t * D;
+      const int64_t hi = live ? len - n + row / p.group + 1 : 0;
+      const int64_t lo = p.window > 0 ? hi - p.window : 0;
+      float m = kLow;
+      uint64_t l2 = 0;  // the sum, even and odd keys
+      bool ok = true;
+      for (int j = 0; j < nt; ++j) {
+        const int slot = j & 3;
+        const int64_t key0 = k0 + static_cast<int64_t>(j) * KT;
+        if (!(ok = wait_warp(&sh.sc_full[slot], (j >> 2) & 1, p.status, 77))) break;
+        if (!(ok = wait_warp(&sh.s_full[t], j & 1, p.status, 78))) break;
+        tc_fence_after();
+        // keys [from, to) of the tile are seen
+        const int from = static_cast<int>(max(lo - key0, static_cast<int64_t>(0)));
+        const int upto = static_cast<int>(min(max(hi - key0, static_cast<int64_t>(0)),
+                                              static_cast<int64_t>(KT)));
+        const bool mask = __any_sync(0xffffffffu, from > 0 || upto < KT);
+        const float top = mask ? row_max<true>(ts, rs, sh.ks[slot], from, upto)
+                               : row_max<false>(ts, rs, sh.ks[slot], from, upto);
+        if (__any_sync(0xffffffffu, top > m + kSlack)) {
+          const float nm = fmaxf(m, top);
+          const float f = exp2_fast(m - nm);
+          m = nm;
+          l2 = mul2(l2, pack2(f, f));
+          if (j > 0) {
+            if (!(ok = wait_warp(&sh.pv_done[t], (j - 1) & 1, p.status, 79))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              float o[16];
+              uint32_t w[16];
+              tmem_ld_32x32b_x16(to + 16 * c, o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * f);
+              tmem_st_x16(to + 16 * c, w);
+            }
+          }
+        }
+        if (mask)
+          row_weights<true>(ts, rs, m, sh.ks[slot], sh.vf[slot], from, upto, l2);
+        else
+          row_weights<false>(ts, rs, m, sh.ks[slot], sh.vf[slot], from, upto, l2);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[t]);
+      }
+      // ------------------------------------------------------------------- result
+      if (ok && nt > 0) ok = wait_warp(&sh.pv_done[t], (nt - 1) & 1, p.status, 80);
       tc_fence_after();
-      // keys [from, to) of the tile are seen
-      const int from = static_cast<int>(max(lo - key0, static_cast<int64_t>(0)));
-      const int upto = static_cast<int>(min(max(hi - key0, static_cast<int64_t>(0)),
-                                            static_cast<int64_t>(KT)));
-      const bool mask = __any_sync(0xffffffffu, from > 0 || upto < KT);
-      float top = ninf;
-#pragma unroll 1
-      for (int c = 0; c < KT / 32; ++c) {
-        float s[32];
-        tmem_ld_32x32b_x32(ts + 32 * c, s);
-        if (mask) {
+      const float vmax = __int_as_float(sh.vmax);
+      float la, lb;
+      unpack2(l2, la, lb);
+      const float l = la + lb;
+      const float norm = (single ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f) * (vmax / kPScale);
+      const int64_t slot = (static_cast<int64_t>(part) * p.tokens + tok) * p.heads + head;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) s[i] = ((seen(from, upto, c) >> i) & 1u) ? s[i] : ninf;
+      for (int c = 0; c < D / 16; ++c) {
+        float o[16];
+        __syncwarp();
+        if (nt > 0) {
+          tmem_ld_32x32b_x16(to + 16 * c, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = 0.0f;
         }
+        if (live && single) {
+          T* at = static_cast<T*>(p.out) + tok * p.ldo + head * D + 16 * c;
+          uint4 v[2];
+          T* w = reinterpret_cast<T*>(v);
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          float x = s[16 * g];
+          for (int i = 0; i < 16; ++i) w[i] = from_float<T>(o[i] * norm);
+          reinterpret_cast<uint4*>(at)[0] = v[0];
+          reinterpret_cast<uint4*>(at)[1] = v[1];
+        } else if (live) {
+          float4* at = reinterpret_cast<float4*>(p.part_o + slot * D + 16 * c);
 #pragma unroll
-          for (int i = 1; i < 16; ++i) x = fmaxf(x, s[16 * g + i]);
-          top = fmaxf(top, x * (rs * sh.ks[slot][2 * c + g]));
-        }
-      }
-      if (__any_sync(0xffffffffu, top > m + kSlack)) {
-        const float nm = fmaxf(m, top);
-        const float f = exp2_fast(m - nm);
-        m = nm;
-        l2 = mul2(l2, pack2(f, f));
-        if (j > 0) {
-          if (!(ok = wait_warp(&sh.pv_done[t], (j - 1) & 1, p.status, 79))) break;
-          tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            float o[16];
-            uint32_t w[16];
-            tmem_ld_32x32b_x16(to + 16 * c, o);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * f);
-            tmem_st_x16(to + 16 * c, w);
-          }
+          for (int i = 0; i < 4; ++i)
+            at[i] = make_float4(o[4 * i] * norm, o[4 * i + 1] * norm, o[4 * i + 2] * norm,
+                                o[4 * i + 3] * norm);
         }
       }
-      const uint64_t nm2 = pack2(-m, -m);
-#pragma unroll 1
-      for (int c = 0; c < KT / 32; ++c) {
-        float s[32];
-        uint32_t w[16];
-        tmem_ld_32x32b_x32(ts + 32 * c, s);
-        const uint32_t bits = mask ? seen(from, upto, c) : 0xFFFFFFFFu;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const float f = rs * sh.ks[slot][2 * c + g], vf = sh.vf[slot][2 * c + g];
-          const uint64_t f2 = pack2(f, f), vf2 = pack2(vf, vf);
-#pragma unroll
-          for (int i = 16 * g; i < 16 * g + 16; i += 2) {
-            float x0, x1, y0, y1;
-            unpack2(fma2(pack2(s[i], s[i + 1]), f2, nm2), x0, x1);
-            if (mask) {
-              x0 = (bits >> i) & 1u ? x0 : ninf;
-              x1 = (bits >> (i + 1)) & 1u ? x1 : ninf;
-            }
-            const uint64_t e = pack2(exp2_fast(x0), exp2_fast(x1));
-            l2 = add2(l2, e);
-            unpack2(mul2(e, vf2), y0, y1);
-            if (mask) {  // 0 times the scale of a block that holds a NaN is not 0
-              y0 = (bits >> i) & 1u ? y0 : 0.0f;
-              y1 = (bits >> (i + 1)) & 1u ? y1 : 0.0f;
-            }
-            const __half2 h = __floats2half2_rn(y0, y1);
-            w[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-        }
-        tmem_st_x16(ts + 16 * c, w);
+      if (live) {
+        if (!single)
+          p.part_ml[slot] = make_float2(m, l);
+        else if (p.lse != nullptr)
+          p.lse[tok * p.heads + head] =
+              l == 0.0f ? __uint_as_float(0xFF800000u) : (m + log2f(l)) * kLn2;
       }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.p_full[t]);
-    }
-    // ------------------------------------------------------------------- result
-    if (ok && nt > 0) ok = wait_warp(&sh.pv_done[t], (nt - 1) & 1, p.status, 80);
-    tc_fence_after();
-    float la, lb;
-    unpack2(l2, la, lb);
-    const float l = la + lb;
-    const float norm = (single ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f) * (vmax / kPScale);
-    const int64_t tok = q0 + (live ? row : 0) / p.group;
-    const int head = kvh * p.group + static_cast<int>((live ? row : 0) % p.group);
-    const int64_t slot = (static_cast<int64_t>(part) * p.tokens + tok) * p.heads + head;
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) {
-      float o[16];
-      __syncwarp();
-      if (nt > 0) {
-        tmem_ld_32x32b_x16(to + 16 * c, o);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = 0.0f;
-      }
-      if (live && single) {
-        T* at = static_cast<T*>(p.out) + tok * p.ldo + head * D + 16 * c;
-        uint4 v[2];
-        T* w = reinterpret_cast<T*>(v);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = from_float<T>(o[i] * norm);
-        reinterpret_cast<uint4*>(at)[0] = v[0];
-        reinterpret_cast<uint4*>(at)[1] = v[1];
-      } else if (live) {
-        float4* at = reinterpret_cast<float4*>(p.part_o + slot * D + 16 * c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          at[i] = make_float4(o[4 * i] * norm, o[4 * i + 1] * norm, o[4 * i + 2] * norm,
-                              o[4 * i + 3] * norm);
-      }
-    }
-    if (live) {
-      if (!single)
-        p.part_ml[slot] = make_float2(m, l);
-      else if (p.lse != nullptr)
-        p.lse[tok * p.heads + head] =
-            l == 0.0f ? __uint_as_float(0xFF800000u) : (m + log2f(l)) * kLn2;
-    }
     }
   }
   tc_fence_before();
