@@ -7,8 +7,14 @@
 // of the dimensions inside a fragment is free as long as q's agrees, so lane
 // (r, c) = (lane / 4, lane % 4) takes bytes 16 c .. of token r for the scores
 // and bytes r * head_dim / 8 .. of tokens 2c, 2c + 1, 2c + 8, 2c + 9 for the
-// values.  Nothing is staged in shared memory.  A byte becomes a half exactly:
-// (code + 128) under the exponent of 1024 is 1152 + code, minus 1152.
+// values.  Nothing is staged in shared memory.  A byte becomes a half exactly, in
+// two ways.  Values: u = code + 128 under the exponent of 1024 is 1152 + code,
+// minus 1152.  Keys: u in the low bits of a half is the subnormal number u 2^-24,
+// which the tensor cores take as it is, and the 128 is taken off the sum instead,
+// q . k = 2^24 (q . u) - 128 sum(q); that saves the subtraction of every pair and
+// costs two bits of the fp32 sum's 24 (u <= 255 against |code| <= 127), nothing
+// beside the rounding of a probability.  For the values it would cost those bits
+// where an output is near 0 beside large values, so they keep the subtraction.
 //
 // Keys and values are the wide operand (16 tokens, or 16 dimensions, a
 // product), the queries the narrow one (8 rows), because a decoding step has
@@ -30,8 +36,8 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kMaxPages = 256;        // pages of a chunk (4096 keys, blocks of 16)
 
+// Bytes 0 and 2, and 1 and 3, of four codes, as halves.
 __device__ __forceinline__ void halves_of(uint32_t w, uint32_t& even, uint32_t& odd) {
-  // bytes 0 and 2, bytes 1 and 3, each + 128 under 0x6400, minus 1152
   const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
   const uint32_t e = (w & 0x00FF00FFu) ^ 0x64806480u;
   const uint32_t o = ((w >> 8) & 0x00FF00FFu) ^ 0x64806480u;
@@ -39,6 +45,11 @@ __device__ __forceinline__ void halves_of(uint32_t w, uint32_t& even, uint32_t& 
   const __half2 oh = __hsub2(*reinterpret_cast<const __half2*>(&o), off);
   even = *reinterpret_cast<const uint32_t*>(&eh);
   odd = *reinterpret_cast<const uint32_t*>(&oh);
+}
+// The same, each + 128 and times 2^-24.
+__device__ __forceinline__ void biased_halves_of(uint32_t w, uint32_t& even, uint32_t& odd) {
+  even = (w & 0x00FF00FFu) ^ 0x00800080u;
+  odd = ((w >> 8) & 0x00FF00FFu) ^ 0x00800080u;
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -64,10 +75,10 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
   constexpr int KS = D / 16;   // k steps of the scores = 16-row tiles of the output
   constexpr int KV = D / 64;   // 16-byte loads of a key a lane; value loads are 4 of D / 8 bytes
   constexpr int OLD = D + 4;   // row stride of the joined output in shared memory
-  __shared__ int s_page[kMaxPages];
+  __shared__ int64_t s_base[kMaxPages];
   __shared__ float s_ks[kMaxPages], s_vs[kMaxPages];
   __shared__ __align__(16) __half s_q[ROWS][D];
-  __shared__ float s_rs[ROWS];
+  __shared__ float s_rs[ROWS], s_qs[ROWS];
   __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
   __shared__ float s_o[kWarps / 2][ROWS][OLD];
 
@@ -107,7 +118,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
       note_status(p.status, PIQ_ERR_INVALID_ARG, b);
       pg = 0;
     }
-    s_page[i] = pg;
+    s_base[i] = (static_cast<int64_t>(pg) * p.kv_heads + kvh) * p.block * D;
     s_ks[i] = ks;
     s_vs[i] = vs;
   }
@@ -129,21 +140,29 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
     }
     amax = warp_max(amax);
     if (__any_sync(0xffffffffu, nan)) amax = __uint_as_float(0x7FC00000u);
-    float mul;
+    float mul, sum = 0.0f;
     const float undo = row_exponent<T>(amax, mul);
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) {
-      const float h = undo == undo ? v[j] * mul : 0.0f;
-      s_q[i][32 * j + lane] = __float2half_rn(h);
+      const __half h = __float2half_rn(undo == undo ? v[j] * mul : 0.0f);
+      s_q[i][32 * j + lane] = h;
+      sum += __half2float(h);
     }
-    if (lane == 0) s_rs[i] = undo * p.scale2;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) {
+      s_rs[i] = undo * p.scale2;
+      s_qs[i] = -128.0f * sum;
+    }
   }
   __syncthreads();
 
   // -------------------------------------------------------------- fragments of q
   uint32_t qf[NT][KS][2];
-  float rs[NT][2];
-  int64_t hi[NT][2];  // keys that rows 2c, 2c + 1 see: j < hi
+  float rs[NT][2], qs[NT][2];
+  int hi[NT][2];  // keys of the chunk that rows 2c, 2c + 1 see: j < hi
+  const int nkeys = static_cast<int>(k1 - k0);
+  const int window = static_cast<int>(min(p.window, static_cast<int64_t>(INT32_MAX)));
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -157,13 +176,17 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
     for (int e = 0; e < 2; ++e) {
       const int64_t row = row0 + 8 * t + 2 * c + e;
       rs[t][e] = s_rs[8 * t + 2 * c + e];
-      hi[t][e] = row < rows ? len - n + row / p.group + 1 : 0;
+      qs[t][e] = s_qs[8 * t + 2 * c + e];
+      hi[t][e] = row < rows ? static_cast<int>(len - n + row / p.group + 1 - k0) : 0;
     }
   }
   // tiles in which every row sees every key need no masks
   const int64_t last_row = min(row0 + ROWS, rows) - 1;
-  const int64_t all_lo = p.window > 0 ? len - n + last_row / p.group + 1 - p.window : 0;
-  const int64_t all_hi = row0 + ROWS <= rows ? len - n + row0 / p.group + 1 : 0;
+  const int all_lo = p.window > 0
+                         ? static_cast<int>(max(len - n + last_row / p.group + 1 - p.window - k0,
+                                                static_cast<int64_t>(0)))
+                         : 0;
+  const int all_hi = row0 + ROWS <= rows ? static_cast<int>(len - n + row0 / p.group + 1 - k0) : 0;
 
   float m[NT][2], l[NT][2], o[NT][KS][4];
   float vmax = 0.0f;
@@ -176,35 +199,34 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
   }
 
   // ------------------------------------------------------------- the keys, 16 a step
-  const int ntiles = static_cast<int>(k1 > k0 ? (k1 - k0 + 15) / 16 : 0);
-  const int tpb = p.block / 16;
+  const int ntiles = (nkeys + 15) / 16;
+  const int shift = __ffs(p.block) - 5;  // log2 of the tiles of a page
+  const int in_page = (1 << shift) - 1;
+  const int8_t* const kbase = p.kc + r * D + 16 * c;
+  const int8_t* const vbase = p.vc + 2 * c * D + r * (D / 8);
   uint4 kr[2][KV];
   uint32_t vr[4][D / 32];
-  auto base_of = [&](int tile) {
-    return (static_cast<int64_t>(s_page[tile / tpb]) * p.kv_heads + kvh) * p.block * D +
-           (tile % tpb) * 16 * D;
-  };
   auto load_k = [&](int tile) {
-    const int8_t* kb = p.kc + base_of(tile);
+    const int8_t* at = kbase + (s_base[tile >> shift] + (tile & in_page) * (16 * D));
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int j = 0; j < KV; ++j)
-        kr[h][j] = __ldg(reinterpret_cast<const uint4*>(kb + (r + 8 * h) * D + 64 * j + 16 * c));
+        kr[h][j] = __ldg(reinterpret_cast<const uint4*>(at + 8 * h * D + 64 * j));
   };
   auto load_v = [&](int tile) {
-    const int8_t* vb = p.vc + base_of(tile);
+    const int8_t* at = vbase + (s_base[tile >> shift] + (tile & in_page) * (16 * D));
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
-      const int8_t* at = vb + (2 * c + (h & 1) + 8 * (h >> 1)) * D + r * (D / 8);
+      const int8_t* a = at + ((h & 1) + 8 * (h >> 1)) * D;
       if constexpr (D == 128) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(at));
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(a));
         vr[h][0] = x.x;
         vr[h][1] = x.y;
         vr[h][2] = x.z;
         vr[h][3] = x.w;
       } else {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(at));
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(a));
         vr[h][0] = x.x;
         vr[h][1] = x.y;
       }
@@ -214,8 +236,9 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
     load_k(warp);
     load_v(warp);
   }
+#pragma unroll 1
   for (int tile = warp; tile < ntiles; tile += kWarps) {
-    const int64_t key0 = k0 + 16 * tile;
+    const int key0 = 16 * tile;
     float s[NT][4] = {};
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -223,34 +246,42 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
       const uint32_t x0 = ks % 4 == 0 ? w0.x : ks % 4 == 1 ? w0.y : ks % 4 == 2 ? w0.z : w0.w;
       const uint32_t x1 = ks % 4 == 0 ? w1.x : ks % 4 == 1 ? w1.y : ks % 4 == 2 ? w1.z : w1.w;
       uint32_t a0, a1, a2, a3;
-      halves_of(x0, a0, a2);
-      halves_of(x1, a1, a3);
+      biased_halves_of(x0, a0, a2);
+      biased_halves_of(x1, a1, a3);
 #pragma unroll
       for (int t = 0; t < NT; ++t) mma_f16(s[t], a0, a1, a2, a3, qf[t][ks][0], qf[t][ks][1]);
     }
-    const float kscale = s_ks[tile / tpb], vscale = s_vs[tile / tpb];
+    const float kscale = s_ks[tile >> shift], vscale = s_vs[tile >> shift];
     if (tile + kWarps < ntiles) load_k(tile + kWarps);
 
-    // scores in log2 units, masked
+    // scores in log2 units
     bool over = false;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
+      const float f0 = rs[t][0] * kscale, f1 = rs[t][1] * kscale;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[t][e] *= rs[t][e & 1] * kscale;
-      if (key0 < all_lo || key0 + 16 > all_hi) {
+      for (int e = 0; e < 4; ++e)
+        s[t][e] = fmaf(s[t][e], 0x1p24f, qs[t][e & 1]) * (e & 1 ? f1 : f0);
+    }
+    const bool masked = key0 < all_lo || key0 + 16 > all_hi;
+    if (masked) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int64_t j = key0 + r + 8 * (e >> 1), h = hi[t][e & 1];
-          const bool see = j < h && (p.window == 0 || j >= h - p.window);
+          const int j = key0 + r + 8 * (e >> 1), h = hi[t][e & 1];
+          const bool see = j < h && (window == 0 || j >= h - window);
           if (!see) s[t][e] = __uint_as_float(0xFF800000u);
         }
-      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
       over |= fmaxf(s[t][0], s[t][2]) > m[t][0] + kSlack;
       over |= fmaxf(s[t][1], s[t][3]) > m[t][1] + kSlack;
     }
-    float fresh = vscale > vmax ? vscale : vmax;
-    if (__any_sync(0xffffffffu, over) || fresh != vmax) {
+    if (__any_sync(0xffffffffu, over || vscale > vmax)) {
       // the maximum (or the largest value scale) moves: what was summed is rescaled
+      const float fresh = fmaxf(vscale, vmax);
       const float fv = vmax > 0.0f ? vmax / fresh : 0.0f;
       vmax = fresh;
 #pragma unroll
@@ -279,7 +310,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
     }
     // probabilities; those of the values carry the block's scale (NaN scales stay NaN,
     // but only where a key is seen)
-    const float vf = vmax > 0.0f ? kPScale * (vscale / vmax) : (vscale == vscale ? 0.0f : vscale);
+    const float vf = vmax > 0.0f ? __fdividef(kPScale * vscale, vmax) : (vscale == vscale ? 0.0f : vscale);
     uint32_t pb[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -289,7 +320,12 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
         const float p1 = exp2_fast(s[t][2 * h + 1] - m[t][1]);
         l[t][0] += p0;
         l[t][1] += p1;
-        const __half2 ph = __floats2half2_rn(p0 == 0.0f ? 0.0f : p0 * vf, p1 == 0.0f ? 0.0f : p1 * vf);
+        float y0 = p0 * vf, y1 = p1 * vf;
+        if (masked) {
+          y0 = p0 == 0.0f ? 0.0f : y0;
+          y1 = p1 == 0.0f ? 0.0f : y1;
+        }
+        const __half2 ph = __floats2half2_rn(y0, y1);
         pb[t][h] = transpose8x8(*reinterpret_cast<const uint32_t*>(&ph));
       }
     }
@@ -309,7 +345,6 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
     }
     if (tile + kWarps < ntiles) load_v(tile + kWarps);
   }
-
   // --------------------------------------------------------------- join the warps
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -384,11 +419,15 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
   }
 }
 
-// Joins the chunks of one (token, head): the CTA's warps take chunks in turn.
+// Joins the chunks of one (token, head): the largest maximum first, then every
+// warp adds chunks of its own, the loads of several under way at once.
+constexpr int kJoinWarps = 8;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(128) kv8_join_kernel(Kv8Attn p) {
-  __shared__ float s_top[4], s_sum[4];
-  __shared__ float s_o[4][D];
+__global__ void __launch_bounds__(32 * kJoinWarps) kv8_join_kernel(Kv8Attn p) {
+  constexpr int V = D / 32;  // values a lane
+  __shared__ float s_top[kJoinWarps], s_sum[kJoinWarps];
+  __shared__ float s_o[kJoinWarps][D];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -406,39 +445,50 @@ __global__ void __launch_bounds__(128) kv8_join_kernel(Kv8Attn p) {
   if (nc <= 1) return;  // written by its only chunk
   const int64_t stride = p.tokens * p.heads;
   const float2* ml = p.part_ml + t * p.heads + head;
-  const float* po = p.part_o + (t * p.heads + head) * D;
-  float top = kLow, sum = 0.0f, o[D / 32] = {};
-  for (int i = warp; i < nc; i += 4) {
-    const float2 x = ml[i * stride];
-    const float nt = fmaxf(top, x.x);
-    const float fo = exp2_fast(top - nt), fx = exp2_fast(x.x - nt);
-    top = nt;
-    sum = sum * fo + x.y * fx;
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) o[j] = o[j] * fo + po[i * stride * D + 32 * j + lane] * fx;
-  }
-  if (lane == 0) {
-    s_top[warp] = top;
-    s_sum[warp] = sum;
-  }
-#pragma unroll
-  for (int j = 0; j < D / 32; ++j) s_o[warp][32 * j + lane] = o[j];
+  const float* po = p.part_o + (t * p.heads + head) * D + V * lane;
+  float top = kLow;
+  for (int i = threadIdx.x; i < nc; i += 32 * kJoinWarps) top = fmaxf(top, ml[i * stride].x);
+  top = warp_max(top);
+  if (lane == 0) s_top[warp] = top;
   __syncthreads();
-  float all = kLow, total = 0.0f;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) all = fmaxf(all, s_top[w]);
+  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_top[w]);
+  float sum = 0.0f, o[V] = {};
+#pragma unroll 4
+  for (int i = warp; i < nc; i += kJoinWarps) {
+    const float2 x = ml[i * stride];
+    const float f = exp2_fast(x.x - top);
+    const float* at = po + i * stride * D;
+    if constexpr (V == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(at);
+      o[0] = fmaf(v.x, f, o[0]);
+      o[1] = fmaf(v.y, f, o[1]);
+      o[2] = fmaf(v.z, f, o[2]);
+      o[3] = fmaf(v.w, f, o[3]);
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(at);
+      o[0] = fmaf(v.x, f, o[0]);
+      o[1] = fmaf(v.y, f, o[1]);
+    }
+    sum = fmaf(x.y, f, sum);
+  }
+  if (lane == 0) s_sum[warp] = sum;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) total += s_sum[w] * exp2_fast(s_top[w] - all);
+  for (int j = 0; j < V; ++j) s_o[warp][V * lane + j] = o[j];
+  __syncthreads();
+  float total = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) total += s_sum[w];
   const float norm = total == 0.0f ? 0.0f : 1.0f / total;
-  for (int d = threadIdx.x; d < D; d += 128) {
+  for (int d = threadIdx.x; d < D; d += 32 * kJoinWarps) {
     float x = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) x += s_o[w][d] * exp2_fast(s_top[w] - all);
+    for (int w = 0; w < kJoinWarps; ++w) x += s_o[w][d];
     static_cast<T*>(p.out)[t * p.ldo + head * D + d] = from_float<T>(x * norm);
   }
   if (threadIdx.x == 0 && p.lse != nullptr)
     p.lse[t * p.heads + head] =
-        total == 0.0f ? __uint_as_float(0xFF800000u) : (all + log2f(total)) * kLn2;
+        total == 0.0f ? __uint_as_float(0xFF800000u) : (top + log2f(total)) * kLn2;
 }
 
 // Keys a chunk: enough CTAs for two waves of two a multiprocessor, but no
@@ -504,7 +554,7 @@ template <typename T, int D>
 int launch_join(const Kv8Attn& p, cudaStream_t stream) {
   note_launch();
   return launch_pdl(kv8_join_kernel<T, D>, dim3(static_cast<unsigned>(p.tokens), p.heads),
-                    dim3(128), 0, stream, p) == cudaSuccess
+                    dim3(32 * kJoinWarps), 0, stream, p) == cudaSuccess
              ? PIQ_OK
              : PIQ_ERR_CUDA;
 }
