@@ -473,7 +473,8 @@ int piq_kv8_read(const int8_t* k_codes, const int8_t* v_codes, const float* k_sc
  *           batch: they size the launch and the workspace (a sequence above
  *           them is an error: its rows are NaN).
  *           max_len <= 2^26.
- *   heads   a multiple of kv_heads, at most 256 kv_heads; tokens <= 2^24.
+ *   heads   a multiple of kv_heads, at most 256 kv_heads; tokens <= 2^24 and
+ *           tokens * heads < 2^31 - 256.
  * Queries of bf16 are scaled by a power of two a row and used in fp16, exact for
  * values down to 2^-14 of the row's largest; probabilities are used in fp16
  * times 2^7, relative to the largest v_scale and probability in sight.  Sums

@@ -7,7 +7,11 @@
 // of the dimensions inside a fragment is free as long as q's agrees, so lane
 // (r, c) = (lane / 4, lane % 4) takes bytes 16 c .. of token r for the scores
 // and bytes r * head_dim / 8 .. of tokens 2c, 2c + 1, 2c + 8, 2c + 9 for the
-// values.  Nothing is staged in shared memory.  A byte becomes a half exactly, in
+// values.  A lane copies its own pieces into a ring of its warp's in shared memory
+// (asynchronously, 12 KB a warp, each piece where its lane reads it back: no bank
+// conflicts, no barriers), which keeps up to 190 KB of a multiprocessor's reads
+// under way; loads into registers kept 50 KB and ran at 57% of the memory's rate.
+// A byte becomes a half exactly, in
 // two ways.  Values: u = code + 128 under the exponent of 1024 is 1152 + code,
 // minus 1152.  Keys: u in the low bits of a half is the subnormal number u 2^-24,
 // which the tensor cores take as it is, and the 128 is taken off the sum instead,
@@ -26,6 +30,7 @@
 // exceeds it by 2^8: at most 2^15, and what is more than 2^31 below the largest
 // is lost.  The sum of p stays in fp32.
 #include <algorithm>
+#include <atomic>
 
 #include "kv8_attn.cuh"
 
@@ -34,6 +39,7 @@ namespace piq {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kRing = 12 * 1024;      // bytes a warp: 3 stages of 16 keys and values of 128 dimensions
 constexpr int kMaxPages = 256;        // pages of a chunk (4096 keys, blocks of 16)
 
 // Bytes 0 and 2, and 1 and 3, of four codes, as halves.
@@ -74,13 +80,17 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
   constexpr int ROWS = 8 * NT;
   constexpr int KS = D / 16;   // k steps of the scores = 16-row tiles of the output
   constexpr int KV = D / 64;   // 16-byte loads of a key a lane; value loads are 4 of D / 8 bytes
+  constexpr int STAGE = 32 * D;            // bytes of 16 keys and values
+  constexpr int STAGES = kRing / STAGE;
   constexpr int OLD = D + 4;   // row stride of the joined output in shared memory
   __shared__ int64_t s_base[kMaxPages];
   __shared__ float s_ks[kMaxPages], s_vs[kMaxPages];
   __shared__ __align__(16) __half s_q[ROWS][D];
   __shared__ float s_rs[ROWS], s_qs[ROWS];
   __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
-  __shared__ float s_o[kWarps / 2][ROWS][OLD];
+  extern __shared__ __align__(16) uint8_t ring[];  // the warps' rings, then the join's buffer
+  float(*s_o)[ROWS][OLD] = reinterpret_cast<float(*)[ROWS][OLD]>(ring);
+  static_assert(sizeof(float) * (kWarps / 2) * ROWS * OLD <= kWarps * kRing, "join buffer");
 
   pdl_launch_dependents();
   pdl_wait();
@@ -90,26 +100,39 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
   const int row_groups = static_cast<int>(gridDim.x) / p.kv_heads;
   const int kvh = blockIdx.x / row_groups, rg = blockIdx.x % row_groups;
   const int part = blockIdx.y;
-  const int64_t q0 = __ldg(p.cu + b), q1 = __ldg(p.cu + b + 1), len = __ldg(p.lens + b);
-  const int64_t n = q1 - q0;
-  if (n == 0) return;
+  const int64_t q0 = __ldg(p.cu + b), q1 = __ldg(p.cu + b + 1), seq_len = __ldg(p.lens + b);
+  if (q0 == q1) return;
   T* out = static_cast<T*>(p.out);
-  if (bad_lengths<T, D>(p, b, q0, q1, len, blockIdx.x == 0 && part == 0)) return;
-  const int64_t rows = n * p.group;
-  const int64_t row0 = static_cast<int64_t>(rg) * ROWS;
+  if (bad_lengths<T, D>(p, b, q0, q1, seq_len, blockIdx.x == 0 && part == 0)) return;
+  const int n = static_cast<int>(q1 - q0), len = static_cast<int>(seq_len);
+  const int rows = n * p.group;
+  const int row0 = rg * ROWS;
   if (row0 >= rows) return;
-  // keys of this chunk: chunks are counted from the block of the first key in sight
-  const int64_t first = first_key(len, n, p.window);
-  const int64_t origin = first / p.block * p.block;
-  const int64_t k0 = origin + part * p.chunk;
+  const int origin = first_block_key(len, n, p.window, p.block);
+  const int k0 = origin + part * p.chunk;
   if (k0 >= len) return;
-  const int64_t k1 = min(k0 + p.chunk, len);
+  const int nkeys = min(p.chunk, len - k0);
   const bool single = len - origin <= p.chunk;  // this CTA has all the sequence's keys
+  const int shift = __ffs(p.block) - 1;
 
   // -------------------------------------------------- pages and scales, queries
-  const int npages = static_cast<int>(k1 > k0 ? (k1 - k0 + p.block - 1) / p.block : 0);
+  // The rows' values are asked for first, the page table's entries and their scales
+  // next: the waits overlap.
+  constexpr int QW = (ROWS + kWarps - 1) / kWarps;  // rows a warp
+  float qv[QW][D / 32];
+#pragma unroll
+  for (int i = 0; i < QW; ++i) {
+    const unsigned row = row0 + warp + i * kWarps;
+    const unsigned tok = row / p.group, head = row - tok * p.group;
+    const T* src = static_cast<const T*>(p.q) + (q0 + tok) * p.ldq + (kvh * p.group + head) * D;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j)
+      qv[i][j] = row < static_cast<unsigned>(rows) ? to_float(__ldg(src + 32 * j + lane)) : 0.0f;
+  }
+  const int npages = (nkeys + p.block - 1) >> shift;
+  const int32_t* table = p.table + b * p.ldt + (k0 >> shift);
   for (int i = threadIdx.x; i < npages; i += blockDim.x) {
-    int pg = __ldg(p.table + b * p.ldt + k0 / p.block + i);
+    int pg = __ldg(table + i);
     float ks = __uint_as_float(0x7FC00000u), vs = ks;
     if (pg >= 0 && pg < p.pages) {
       ks = __ldg(p.ks + static_cast<int64_t>(pg) * p.kv_heads + kvh);
@@ -122,47 +145,71 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
     s_ks[i] = ks;
     s_vs[i] = vs;
   }
-  for (int i = warp; i < ROWS; i += kWarps) {
-    const int64_t row = row0 + i;
-    float v[D / 32];
+#pragma unroll
+  for (int i = 0; i < QW; ++i) {
     float amax = 0.0f;
     bool nan = false;
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) {
-      v[j] = 0.0f;
-      if (row < rows) {
-        const int64_t t = q0 + row / p.group;
-        const int head = kvh * p.group + static_cast<int>(row % p.group);
-        v[j] = to_float(static_cast<const T*>(p.q)[t * p.ldq + head * D + 32 * j + lane]);
-      }
-      amax = fmaxf(amax, fabsf(v[j]));
-      nan |= !(v[j] == v[j]);
+      amax = fmaxf(amax, fabsf(qv[i][j]));
+      nan |= !(qv[i][j] == qv[i][j]);
     }
     amax = warp_max(amax);
     if (__any_sync(0xffffffffu, nan)) amax = __uint_as_float(0x7FC00000u);
     float mul, sum = 0.0f;
     const float undo = row_exponent<T>(amax, mul);
+    const int at = warp + i * kWarps;
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) {
-      const __half h = __float2half_rn(undo == undo ? v[j] * mul : 0.0f);
-      s_q[i][32 * j + lane] = h;
+      const __half h = __float2half_rn(undo == undo ? qv[i][j] * mul : 0.0f);
+      s_q[at][32 * j + lane] = h;
       sum += __half2float(h);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) {
-      s_rs[i] = undo * p.scale2;
-      s_qs[i] = -128.0f * sum;
+      s_rs[at] = undo * p.scale2;
+      s_qs[at] = -128.0f * sum;
     }
   }
   __syncthreads();
 
+  // ------------------------------------------------------------- the keys, 16 a step
+  const int ntiles = (nkeys + 15) / 16;
+  const int tshift = shift - 4;  // log2 of the tiles of a page
+  const int in_page = (1 << tshift) - 1;
+  const int8_t* const kbase = p.kc + r * D + 16 * c;
+  const int8_t* const vbase = p.vc + 2 * c * D + r * (D / 8);
+  // stage i of the ring: the key pieces (16 bytes a lane, 512 apart), then the values'
+  uint8_t* const mine = ring + warp * kRing;
+  auto fetch = [&](int tile, int stage) {
+    const int64_t base = s_base[tile >> tshift] + (tile & in_page) * (16 * D);
+    const int8_t *ka = kbase + base, *va = vbase + base;
+    uint8_t* to = mine + stage * STAGE + 16 * lane;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < KV; ++j) cp_async16(to + (h * KV + j) * 512, ka + 8 * h * D + 64 * j);
+    to = mine + stage * STAGE + 16 * D + (D / 8) * lane;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const int8_t* a = va + ((h & 1) + 8 * (h >> 1)) * D;
+      if constexpr (D == 128)
+        cp_async16(to + h * 512, a);
+      else
+        cp_async8(to + h * 256, a);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) {
+    if (warp + i * kWarps < ntiles) fetch(warp + i * kWarps, i);
+    cp_async_commit();
+  }
   // -------------------------------------------------------------- fragments of q
   uint32_t qf[NT][KS][2];
   float rs[NT][2], qs[NT][2];
   int hi[NT][2];  // keys of the chunk that rows 2c, 2c + 1 see: j < hi
-  const int nkeys = static_cast<int>(k1 - k0);
-  const int window = static_cast<int>(min(p.window, static_cast<int64_t>(INT32_MAX)));
+  const int window = p.window;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -174,19 +221,17 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int64_t row = row0 + 8 * t + 2 * c + e;
+      const int row = row0 + 8 * t + 2 * c + e;
       rs[t][e] = s_rs[8 * t + 2 * c + e];
       qs[t][e] = s_qs[8 * t + 2 * c + e];
-      hi[t][e] = row < rows ? static_cast<int>(len - n + row / p.group + 1 - k0) : 0;
+      hi[t][e] = row < rows ? len - n + static_cast<int>(static_cast<unsigned>(row) / p.group) + 1 - k0 : 0;
     }
   }
   // tiles in which every row sees every key need no masks
-  const int64_t last_row = min(row0 + ROWS, rows) - 1;
-  const int all_lo = p.window > 0
-                         ? static_cast<int>(max(len - n + last_row / p.group + 1 - p.window - k0,
-                                                static_cast<int64_t>(0)))
-                         : 0;
-  const int all_hi = row0 + ROWS <= rows ? static_cast<int>(len - n + row0 / p.group + 1 - k0) : 0;
+  const unsigned last_tok = static_cast<unsigned>(min(row0 + ROWS, rows) - 1) / p.group;
+  const unsigned first_tok = static_cast<unsigned>(row0) / p.group;
+  const int all_lo = window > 0 ? max(len - n + static_cast<int>(last_tok) + 1 - window - k0, 0) : 0;
+  const int all_hi = row0 + ROWS <= rows ? len - n + static_cast<int>(first_tok) + 1 - k0 : 0;
 
   float m[NT][2], l[NT][2], o[NT][KS][4];
   float vmax = 0.0f;
@@ -198,48 +243,26 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
     for (int j = 0; j < KS; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.0f;
   }
 
-  // ------------------------------------------------------------- the keys, 16 a step
-  const int ntiles = (nkeys + 15) / 16;
-  const int shift = __ffs(p.block) - 5;  // log2 of the tiles of a page
-  const int in_page = (1 << shift) - 1;
-  const int8_t* const kbase = p.kc + r * D + 16 * c;
-  const int8_t* const vbase = p.vc + 2 * c * D + r * (D / 8);
-  uint4 kr[2][KV];
-  uint32_t vr[4][D / 32];
-  auto load_k = [&](int tile) {
-    const int8_t* at = kbase + (s_base[tile >> shift] + (tile & in_page) * (16 * D));
+  int stage = 0;
+#pragma unroll 1
+  for (int tile = warp; tile < ntiles; tile += kWarps) {
+    const int key0 = 16 * tile;
+    cp_async_wait<STAGES - 2>();
+    {
+      const int next = tile + (STAGES - 1) * kWarps;
+      if (next < ntiles) fetch(next, stage == 0 ? STAGES - 1 : stage - 1);
+      cp_async_commit();
+    }
+    const uint8_t* const kat = mine + stage * STAGE + 16 * lane;
+    const uint8_t* const vat = mine + stage * STAGE + 16 * D + (D / 8) * lane;
+    stage = stage == STAGES - 1 ? 0 : stage + 1;
+    uint4 kr[2][KV];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int j = 0; j < KV; ++j)
-        kr[h][j] = __ldg(reinterpret_cast<const uint4*>(at + 8 * h * D + 64 * j));
-  };
-  auto load_v = [&](int tile) {
-    const int8_t* at = vbase + (s_base[tile >> shift] + (tile & in_page) * (16 * D));
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const int8_t* a = at + ((h & 1) + 8 * (h >> 1)) * D;
-      if constexpr (D == 128) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(a));
-        vr[h][0] = x.x;
-        vr[h][1] = x.y;
-        vr[h][2] = x.z;
-        vr[h][3] = x.w;
-      } else {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(a));
-        vr[h][0] = x.x;
-        vr[h][1] = x.y;
-      }
-    }
-  };
-  if (warp < ntiles) {
-    load_k(warp);
-    load_v(warp);
-  }
-#pragma unroll 1
-  for (int tile = warp; tile < ntiles; tile += kWarps) {
-    const int key0 = 16 * tile;
-    float s[NT][4] = {};
+        kr[h][j] = *reinterpret_cast<const uint4*>(kat + (h * KV + j) * 512);
+    float s[NT][4] = {}, s2[NT][4] = {};  // two chains of products
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       const uint4 w0 = kr[0][ks / 4], w1 = kr[1][ks / 4];
@@ -249,10 +272,10 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
       biased_halves_of(x0, a0, a2);
       biased_halves_of(x1, a1, a3);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) mma_f16(s[t], a0, a1, a2, a3, qf[t][ks][0], qf[t][ks][1]);
+      for (int t = 0; t < NT; ++t)
+        mma_f16(ks & 1 ? s2[t] : s[t], a0, a1, a2, a3, qf[t][ks][0], qf[t][ks][1]);
     }
-    const float kscale = s_ks[tile >> shift], vscale = s_vs[tile >> shift];
-    if (tile + kWarps < ntiles) load_k(tile + kWarps);
+    const float kscale = s_ks[tile >> tshift], vscale = s_vs[tile >> tshift];
 
     // scores in log2 units
     bool over = false;
@@ -261,7 +284,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
       const float f0 = rs[t][0] * kscale, f1 = rs[t][1] * kscale;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        s[t][e] = fmaf(s[t][e], 0x1p24f, qs[t][e & 1]) * (e & 1 ? f1 : f0);
+        s[t][e] = fmaf(s[t][e] + s2[t][e], 0x1p24f, qs[t][e & 1]) * (e & 1 ? f1 : f0);
     }
     const bool masked = key0 < all_lo || key0 + 16 > all_hi;
     if (masked) {
@@ -329,6 +352,21 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
         pb[t][h] = transpose8x8(*reinterpret_cast<const uint32_t*>(&ph));
       }
     }
+    uint32_t vr[4][D / 32];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      if constexpr (D == 128) {
+        const uint4 x = *reinterpret_cast<const uint4*>(vat + h * 512);
+        vr[h][0] = x.x;
+        vr[h][1] = x.y;
+        vr[h][2] = x.z;
+        vr[h][3] = x.w;
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(vat + h * 256);
+        vr[h][0] = x.x;
+        vr[h][1] = x.y;
+      }
+    }
     // keys past the end of the page's tokens: their codes are whatever lies there, times 0
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) {
@@ -343,9 +381,9 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
         for (int t = 0; t < NT; ++t) mma_f16(o[t][2 * w + half], a0, a1, a2, a3, pb[t][0], pb[t][1]);
       }
     }
-    if (tile + kWarps < ntiles) load_v(tile + kWarps);
   }
   // --------------------------------------------------------------- join the warps
+  cp_async_wait<0>();
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -387,15 +425,16 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
     __syncthreads();
   }
   for (int i = warp; i < ROWS; i += kWarps) {
-    const int64_t row = row0 + i;
+    const int row = row0 + i;
     if (row >= rows) break;
     float top = kLow, sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][i]);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) sum += s_l[w][i] * exp2_fast(s_m[w][i] - top);
-    const int64_t t = q0 + row / p.group;
-    const int head = kvh * p.group + static_cast<int>(row % p.group);
+    const unsigned tok = static_cast<unsigned>(row) / p.group;
+    const int64_t t = q0 + tok;
+    const int head = kvh * p.group + static_cast<int>(row - tok * p.group);
     const float norm = single ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
     const int64_t slot = (static_cast<int64_t>(part) * p.tokens + t) * p.heads + head;
 #pragma unroll
@@ -440,8 +479,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv8_join_kernel(Kv8Attn p) {
   if (q0 < 0 || q1 > p.tokens || n > p.max_new || len < n || len > p.max_len ||
       len > p.width * p.block)
     return;  // its rows are NaN already
-  const int64_t origin = first_key(len, n, p.window) / p.block * p.block;
-  const int nc = static_cast<int>((len - origin + p.chunk - 1) / p.chunk);
+  const int span = static_cast<int>(len) -
+                   first_block_key(static_cast<int>(len), static_cast<int>(n), p.window, p.block);
+  const int nc = (span + p.chunk - 1) / p.chunk;
   if (nc <= 1) return;  // written by its only chunk
   const int64_t stride = p.tokens * p.heads;
   const float2* ml = p.part_ml + t * p.heads + head;
@@ -500,18 +540,20 @@ struct AttnPlan {
   bool prompt;       // kv8_prompt.cu
   int nt;            // groups of eight rows a CTA
   int64_t row_groups, chunk;
+  int window;        // 0: none
   int chunks;
 };
 
 AttnPlan plan_attention(int64_t tokens, int heads, int kv_heads, int64_t batch, int64_t max_new, int64_t max_len,
                         int64_t window) {
   AttnPlan a;
+  a.window = window < max_len ? static_cast<int>(window) : 0;  // a wider one hides nothing
   const int64_t rows = std::min(max_new, tokens) * (heads / kv_heads);
   a.prompt = rows > kManyRows;
   a.nt = rows <= 8 ? 1 : 2;
   a.row_groups = std::max<int64_t>(1, ceil_div(rows, 8 * a.nt));
   int64_t span = max_len;  // most keys in sight of a sequence, from a block's (at most 128) start
-  if (window > 0) span = std::min(span, window + max_new + 128);
+  if (a.window > 0) span = std::min(span, window + max_new + 128);
   span = std::max<int64_t>(span, 1);
   if (a.prompt) {
     // whole multiprocessors: split the keys only where the rows leave some idle
@@ -524,7 +566,7 @@ AttnPlan plan_attention(int64_t tokens, int heads, int kv_heads, int64_t batch, 
     return a;
   }
   const int64_t ctas = a.row_groups * kv_heads * batch;
-  const int64_t want = std::max<int64_t>(1, 4 * 148 / ctas);
+  const int64_t want = std::max<int64_t>(1, 2 * 148 / ctas);
   a.chunk = ceil_div(ceil_div(span, want), 128) * 128;
   a.chunk = std::min(std::max(a.chunk, kMinChunk), kMaxChunk);
   a.chunks = static_cast<int>(ceil_div(span, a.chunk));
@@ -534,7 +576,8 @@ AttnPlan plan_attention(int64_t tokens, int heads, int kv_heads, int64_t batch, 
 bool attn_sizes_ok(int64_t tokens, int heads, int kv_heads, int head_dim, int64_t batch,
                    int64_t max_new, int64_t max_len, int window) {
   return tokens >= 0 && tokens <= (int64_t)1 << 24 && kv_heads >= 1 && kv_heads <= 1024 &&
-         heads >= kv_heads && heads % kv_heads == 0 && heads / kv_heads <= 256 && heads <= 65535 &&
+         heads >= kv_heads && heads % kv_heads == 0 && heads / kv_heads <= 256 &&
+         heads <= 65535 && tokens * heads <= INT32_MAX - 256 &&
          (head_dim == 64 || head_dim == 128) && batch >= 1 && batch <= 65535 && max_new >= 0 &&
          max_new <= INT32_MAX && max_len >= 0 && max_len <= (int64_t)1 << 26 && window >= 0;
 }
@@ -568,9 +611,19 @@ int launch_attention(const Kv8Attn& p, const AttnPlan& a, cudaStream_t stream) {
   }
   void (*kern)(Kv8Attn) = a.nt == 1 ? kv8_chunk_kernel<T, D, 1> : kv8_chunk_kernel<T, D, 2>;
   const unsigned gx = static_cast<unsigned>(a.row_groups * p.kv_heads);
+  constexpr int smem = kWarps * kRing;
+  static std::atomic<bool> set[2][64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PIQ_ERR_CUDA;
+  std::atomic<bool>* done = dev < 64 ? &set[a.nt - 1][dev] : nullptr;
+  if (done == nullptr || !done->load(std::memory_order_acquire)) {
+    const int rc = cuda_rc(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    if (rc != PIQ_OK) return rc;
+    if (done != nullptr) done->store(true, std::memory_order_release);
+  }
   note_launch();
-  if (launch_pdl(kern, dim3(gx, a.chunks, p.batch), dim3(32 * kWarps), 0,
-                 stream, p) != cudaSuccess)
+  if (launch_pdl(kern, dim3(gx, a.chunks, p.batch), dim3(32 * kWarps), smem, stream, p) !=
+      cudaSuccess)
     return PIQ_ERR_CUDA;
   return a.chunks == 1 ? PIQ_OK : launch_join<T, D>(p, stream);
 }
@@ -645,10 +698,10 @@ int piq_kv8_attention(const void* q, int dtype, int64_t tokens, int64_t ldq, int
   p.block = block;
   p.group = heads / kv_heads;
   p.scale2 = scale * 1.4426950408889634f;
-  p.window = window;
+  p.window = a.window;
   p.max_new = max_new;
   p.max_len = max_len;
-  p.chunk = a.chunk;
+  p.chunk = static_cast<int>(a.chunk);
   p.chunks = a.chunks;
   p.out = out;
   p.ldo = ldo;

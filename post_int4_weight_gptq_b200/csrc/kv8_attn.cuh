@@ -17,9 +17,9 @@ struct Kv8Attn {
   int64_t pages;
   int batch, heads, kv_heads, block, group;  // group = heads / kv_heads
   float scale2;                              // scale * log2(e)
-  int64_t window;                            // 0: none
+  int window;                                // 0: none
   int64_t max_new, max_len;
-  int64_t chunk;                             // keys a CTA, a multiple of 128
+  int chunk;                                 // keys a CTA, a multiple of 128
   int chunks;                                // most chunks of a sequence
   void* out;
   int64_t ldo;
@@ -34,9 +34,11 @@ constexpr float kLow = -3.0e38f;      // below every score: "no key yet"
 constexpr float kPScale = 128.0f;     // 2^7
 constexpr float kSlack = 8.0f;        // log2 by which a score may pass the maximum
 
-// Keys that some query of the sequence sees: [first, len).
-__device__ __forceinline__ int64_t first_key(int64_t len, int64_t n, int64_t window) {
-  return window > 0 ? max(static_cast<int64_t>(0), len - n + 1 - window) : 0;
+// The block in which the first key that some query sees lies: chunks are counted
+// from its start.  (Lengths are at most 2^26 and rows below 2^31, so positions are
+// 32-bit numbers; 64-bit divisions cost these kernels thousands of cycles.)
+__device__ __forceinline__ int first_block_key(int len, int n, int window, int block) {
+  return window > 0 ? max(0, len - n + 1 - window) & -block : 0;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {

@@ -307,26 +307,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
     b = lo - 1;
   }
   if (b < 0) return;
-  const int64_t q0 = __ldg(p.cu + b), q1 = __ldg(p.cu + b + 1), len = __ldg(p.lens + b);
-  const int64_t n = q1 - q0;
-  const int64_t row0 = (item - (q0 * p.group / kPromptRows + b)) * kPromptRows;
-  if (n == 0) return;
-  if (bad_lengths<T, D>(p, b, q0, q1, len, row0 == 0 && part == 0 && kvh == 0)) return;
-  const int64_t rows = n * p.group;
-  if (row0 >= rows) return;
+  const int64_t q0 = __ldg(p.cu + b), q1 = __ldg(p.cu + b + 1), seq_len = __ldg(p.lens + b);
+  if (q0 == q1) return;
+  const int64_t first_row = (item - (q0 * p.group / kPromptRows + b)) * kPromptRows;
+  if (bad_lengths<T, D>(p, b, q0, q1, seq_len, first_row == 0 && part == 0 && kvh == 0)) return;
+  const int n = static_cast<int>(q1 - q0), len = static_cast<int>(seq_len);
+  const int rows = n * p.group;
+  if (first_row >= rows) return;
+  const int row0 = static_cast<int>(first_row);
   const int nq = rows - row0 > 128 ? 2 : 1;  // tiles with rows in them
   // ------------------------------------------------------------- which keys
-  const int64_t origin = first_key(len, n, p.window) / p.block * p.block;
-  const int64_t c0 = origin + part * p.chunk;
+  const int origin = first_block_key(len, n, p.window, p.block);
+  const int c0 = origin + part * p.chunk;
   if (c0 >= len) return;
-  const int64_t c1 = min(c0 + p.chunk, len);
+  const int c1 = c0 + min(p.chunk, len - c0);
   const bool single = len - origin <= p.chunk;
-  const int64_t last = min(row0 + kPromptRows, rows) - 1;
-  const int64_t see_lo = p.window > 0 ? len - n + row0 / p.group + 1 - p.window : 0;
-  const int64_t see_hi = len - n + last / p.group + 1;
-  const int64_t k0 = max(c0, see_lo & ~static_cast<int64_t>(15));
-  const int64_t k1 = min(c1, see_hi);
-  const int nt = k1 > k0 ? static_cast<int>((k1 - k0 + KT - 1) / KT) : 0;
+  const int first_tok = static_cast<int>(static_cast<unsigned>(row0) / p.group);
+  const int last_tok =
+      static_cast<int>(static_cast<unsigned>(min(row0 + kPromptRows, rows) - 1) / p.group);
+  const int see_lo = p.window > 0 ? max(len - n + first_tok + 1 - p.window, 0) : 0;
+  const int k0 = max(c0, see_lo & ~15);
+  const int k1 = min(c1, len - n + last_tok + 1);
+  const int nt = k1 > k0 ? (k1 - k0 + KT - 1) / KT : 0;
+  const int shift = __ffs(p.block) - 1;
+  const int32_t* table = p.table + b * p.ldt;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -353,10 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
   const uint32_t tmem = sh.tmem;
   // the largest value scale, found by the widening warps
   auto find_vmax = [&]() {
-    const int64_t b0 = k0 / p.block, b1 = (k1 - 1) / p.block;
+    const int b0 = k0 >> shift, b1 = (k1 - 1) >> shift;
     float top = 0.0f;
-    for (int64_t i = b0 + threadIdx.x - 256; i <= b1; i += 128) {
-      const int pg = __ldg(p.table + b * p.ldt + i);
+    for (int i = b0 + static_cast<int>(threadIdx.x) - 256; i <= b1; i += 128) {
+      const int pg = __ldg(table + i);
       if (pg >= 0 && pg < p.pages)
         top = fmaxf(top, __ldg(p.vs + static_cast<int64_t>(pg) * p.kv_heads + kvh));
     }
@@ -431,10 +435,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
     int entry = 0;
     int64_t base = 0;
     float gks = 0.0f, gvs = 0.0f;
-    const int shift = __ffs(p.block) - 1;
-    const int32_t* table = p.table + b * p.ldt;
     auto fetch = [&](int j) {
-      const int64_t k = k0 + static_cast<int64_t>(j) * KT + 16 * (lane & 7);
+      const int k = k0 + j * KT + 16 * (lane & 7);
       entry = k < k1 ? __ldg(table + (k >> shift)) : -2;  // -2: no such keys
     };
     auto look = [&](int j) {
@@ -447,8 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
       } else if (entry != -2) {
         note_status(p.status, PIQ_ERR_INVALID_ARG, b);
       }
-      const int off = static_cast<int>(k0 + static_cast<int64_t>(j) * KT + 16 * (lane & 7)) &
-                      (p.block - 1);
+      const int off = (k0 + j * KT + 16 * (lane & 7)) & (p.block - 1);
       base = ((static_cast<int64_t>(page) * p.kv_heads + kvh) * p.block + off) * D;
     };
     auto load = [&](const int8_t* codes, uint4 (&reg)[PIECES]) {
@@ -505,10 +506,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
     // ------------------------------------------------------------------ softmax
     more_registers<kRegSoftmax>();
     if (warp < 4 * nq) {
-      const int64_t row = row0 + threadIdx.x;
-      const bool live = row < rows;
-      const int64_t tok = q0 + (live ? row : 0) / p.group;
-      const int head = kvh * p.group + static_cast<int>((live ? row : 0) % p.group);
+      const unsigned row = row0 + threadIdx.x;
+      const bool live = row < static_cast<unsigned>(rows);
+      const unsigned rel = (live ? row : 0u) / p.group;
+      const int64_t tok = q0 + rel;
+      const int head = kvh * p.group + static_cast<int>((live ? row : 0u) - rel * p.group);
       const float rs = stage_query<T, D>(
           live ? static_cast<const T*>(p.q) + tok * p.ldq + head * D : nullptr,
           smem + (threadIdx.x >> 7) * L::TILE, threadIdx.x & 127, p.scale2);
@@ -518,21 +520,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
       const int t = warp >> 2;
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t ts = tmem + lanes + t * KT, to = tmem + lanes + 2 * KT + t * D;
-      const int64_t hi = live ? len - n + row / p.group + 1 : 0;
-      const int64_t lo = p.window > 0 ? hi - p.window : 0;
+      const int hi = live ? len - n + static_cast<int>(rel) + 1 : 0;
+      const int lo = p.window > 0 ? hi - p.window : 0;
       float m = kLow;
       uint64_t l2 = 0;  // the sum, even and odd keys
       bool ok = true;
       for (int j = 0; j < nt; ++j) {
         const int slot = j & 3;
-        const int64_t key0 = k0 + static_cast<int64_t>(j) * KT;
+        const int key0 = k0 + j * KT;
         if (!(ok = wait_warp(&sh.sc_full[slot], (j >> 2) & 1, p.status, 77))) break;
         if (!(ok = wait_warp(&sh.s_full[t], j & 1, p.status, 78))) break;
         tc_fence_after();
         // keys [from, to) of the tile are seen
-        const int from = static_cast<int>(max(lo - key0, static_cast<int64_t>(0)));
-        const int upto = static_cast<int>(min(max(hi - key0, static_cast<int64_t>(0)),
-                                              static_cast<int64_t>(KT)));
+        const int from = max(lo - key0, 0), upto = min(max(hi - key0, 0), KT);
         const bool mask = __any_sync(0xffffffffu, from > 0 || upto < KT);
         const float top = mask ? row_max<true>(ts, rs, sh.ks[slot], from, upto)
                                : row_max<false>(ts, rs, sh.ks[slot], from, upto);
