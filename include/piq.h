@@ -428,7 +428,7 @@ int piq_int8_linear(const void* X, int dtype, int64_t tokens, int64_t in, int64_
  *                     page that holds tokens [j block, (j + 1) block) of
  *                     sequence b is block_table[b, j].
  * head_dim is 64 or 128; block is 16, 32, 64 or 128; 1 <= kv_heads <= 1024;
- * 1 <= batch <= 65535; 1 <= pages <= 2^31 - 1. Rows of ragged tensors belong to
+ * 1 <= batch <= 65535; 1 <= pages, pages * kv_heads < 2^31. Rows of ragged tensors belong to
  * sequences by cu (device int32 [batch + 1], non-decreasing): rows cu[b] ..
  * cu[b + 1] - 1 are sequence b's, in order; rows of no sequence are not touched.
  *

@@ -52,20 +52,6 @@ struct GemmArgs {
   int32_t* status;
 };
 
-// mbar_wait with the caller's status words.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int32_t* status,
-                                         int where) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  for (;;) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (global_timer_ns() - t0 > kWaitLimitNs) {
-      note_status(status, PIQ_ERR_TIMEOUT, where);
-      return false;
-    }
-  }
-}
-
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -440,28 +426,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpi, 1)
 }
 
 // -------------------------------------------------------------------- host
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static const EncodeTiledFn fn = [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult qr;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &qr) !=
-            cudaSuccess ||
-        qr != cudaDriverEntryPointSuccess)
-      ptr = nullptr;
-    return reinterpret_cast<EncodeTiledFn>(ptr);
-  }();
-  return fn;
-}
-
 // [rows, cols] int8 with row stride ld as boxes of 128 bytes x box_rows.
 bool code_map(CUtensorMap* map, const int8_t* q, int64_t rows, int64_t cols, int64_t ld,
               int box_rows) {
-  const EncodeTiledFn fn = encode_fn();
+  const EncodeTiledFn fn = tensor_map_encoder();
   if (fn == nullptr) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
@@ -540,6 +508,19 @@ int gemm_t(const int8_t* qx, int64_t ldq, const int8_t* W, int64_t ldw, GemmArgs
 }
 
 }  // namespace
+
+EncodeTiledFn tensor_map_encoder() {
+  static const EncodeTiledFn fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult qr;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &qr) !=
+            cudaSuccess ||
+        qr != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(ptr);
+  }();
+  return fn;
+}
 
 // Tiles of one product.  Many tokens: pairs, on 256-token tiles when those give
 // every pair of multiprocessors work, else on 128-token tiles while they do.

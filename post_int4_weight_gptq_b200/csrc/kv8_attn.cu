@@ -2,23 +2,25 @@
 //
 //   x_j = scale q . (k_scale k_j),  out = sum_j 2^(x_j') v_scale v_j / sum_j 2^(x_j')
 //
-// (x' = x log2 e - running maximum).  The codes go from memory to registers in
-// 16-byte loads, laid out so that they already are matrix fragments: the order
-// of the dimensions inside a fragment is free as long as q's agrees, so lane
-// (r, c) = (lane / 4, lane % 4) takes bytes 16 c .. of token r for the scores
-// and bytes r * head_dim / 8 .. of tokens 2c, 2c + 1, 2c + 8, 2c + 9 for the
-// values.  A lane copies its own pieces into a ring of its warp's in shared memory
-// (asynchronously, 12 KB a warp, each piece where its lane reads it back: no bank
-// conflicts, no barriers), which keeps up to 190 KB of a multiprocessor's reads
-// under way; loads into registers kept 50 KB and ran at 57% of the memory's rate.
-// A byte becomes a half exactly, in
-// two ways.  Values: u = code + 128 under the exponent of 1024 is 1152 + code,
-// minus 1152.  Keys: u in the low bits of a half is the subnormal number u 2^-24,
-// which the tensor cores take as it is, and the 128 is taken off the sum instead,
-// q . k = 2^24 (q . u) - 128 sum(q); that saves the subtraction of every pair and
-// costs two bits of the fp32 sum's 24 (u <= 255 against |code| <= 127), nothing
-// beside the rounding of a probability.  For the values it would cost those bits
-// where an output is near 0 beside large values, so they keep the subtraction.
+// (x' = x log2 e - running maximum).  Every warp has a ring of its own in shared
+// memory, filled by TMA with tiles of 32 keys and values (a copy is issued when the
+// warp has read the stage before; copies into registers kept too few bytes under
+// way, and cp.async of scattered 16-byte pieces took 20 cycles of the shared-memory
+// pipe an instruction).  From there 16-byte reads give matrix fragments as they
+// are, because the order of the dimensions inside a fragment is free as long as q's
+// agrees: lane (r, c) = (lane / 4, lane % 4) takes bytes 16 c .. of a token for the
+// scores, and one eighth of the dimensions of four tokens for the values.  The
+// tokens' places in a tile of 16 and the eighths are permuted so that the swizzled
+// reads of eight lanes meet 32 different banks.
+//
+// A byte becomes a half exactly, in two ways.  Values: u = code + 128 under the
+// exponent of 1024 is 1152 + code, minus 1152.  Keys: u in the low bits of a half is
+// the subnormal number u 2^-24, which the tensor cores take as it is, and the 128 is
+// taken off the sum instead, q . k = 2^24 (q . u) - 128 sum(q); that saves the
+// subtraction of every pair and costs two bits of the fp32 sum's 24 (u <= 255
+// against |code| <= 127), nothing beside the rounding of a probability.  For the
+// values it would cost those bits where an output is near 0 beside large values, so
+// they keep the subtraction.
 //
 // Keys and values are the wide operand (16 tokens, or 16 dimensions, a
 // product), the queries the narrow one (8 rows), because a decoding step has
@@ -31,6 +33,7 @@
 // is lost.  The sum of p stays in fp32.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "kv8_attn.cuh"
 
@@ -38,8 +41,8 @@ namespace piq {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kRing = 12 * 1024;      // bytes a warp: 3 stages of 16 keys and values of 128 dimensions
+constexpr int kWarps = 6;
+constexpr int kRing = 16 * 1024;      // bytes a warp: 2 stages of 32 keys and values of 128 dimensions
 constexpr int kMaxPages = 256;        // pages of a chunk (4096 keys, blocks of 16)
 
 // Bytes 0 and 2, and 1 and 3, of four codes, as halves.
@@ -73,28 +76,45 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
+// The token that row k of a tile of 16 stands for (k < 8; the others are 8 further
+// on).  Rows of 128 bytes (128-byte swizzle): k and k + 1 are four apart, so that
+// their halves of a row lie in other banks.  Rows of 64 (64-byte swizzle, two a
+// line): k and k + 1 lie in other halves of a line, and of the even ones (and the
+// odd ones) two in either half, in lines two apart.
+template <int D>
+__device__ __forceinline__ int token_of(int k) {
+  const int c = k >> 1, odd = k & 1;
+  return D == 128 ? odd * 4 + c : ((c >> 1) * 4 + (c & 1)) ^ (odd * 3);
+}
+
 // NT groups of eight query rows of one kv head (rows are (token, head) pairs,
 // the heads of the group fastest) against one chunk of keys.
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel(Kv8Attn p) {
+__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel(
+    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, Kv8Attn p) {
   constexpr int ROWS = 8 * NT;
   constexpr int KS = D / 16;   // k steps of the scores = 16-row tiles of the output
   constexpr int KV = D / 64;   // 16-byte loads of a key a lane; value loads are 4 of D / 8 bytes
-  constexpr int STAGE = 32 * D;            // bytes of 16 keys and values
+  constexpr int STAGE = 64 * D;            // bytes of 32 keys, then their 32 values
   constexpr int STAGES = kRing / STAGE;
   constexpr int OLD = D + 4;   // row stride of the joined output in shared memory
-  __shared__ int64_t s_base[kMaxPages];
+  __shared__ int s_page[kMaxPages];  // page kv_heads + head
   __shared__ float s_ks[kMaxPages], s_vs[kMaxPages];
   __shared__ __align__(16) __half s_q[ROWS][D];
   __shared__ float s_rs[ROWS], s_qs[ROWS];
   __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
-  extern __shared__ __align__(16) uint8_t ring[];  // the warps' rings, then the join's buffer
+  __shared__ uint64_t full[kWarps][STAGES];
+  extern __shared__ uint8_t ring_raw[];  // the warps' rings, then the join's buffer
+  uint8_t* const ring = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(ring_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   float(*s_o)[ROWS][OLD] = reinterpret_cast<float(*)[ROWS][OLD]>(ring);
   static_assert(sizeof(float) * (kWarps / 2) * ROWS * OLD <= kWarps * kRing, "join buffer");
 
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane < STAGES) mbar_init(&full[warp][lane], 1);
+  fence_mbar_init();
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, c = lane & 3;
   const int b = blockIdx.z;
   const int row_groups = static_cast<int>(gridDim.x) / p.kv_heads;
@@ -122,7 +142,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
   float qv[QW][D / 32];
 #pragma unroll
   for (int i = 0; i < QW; ++i) {
-    const unsigned row = row0 + warp + i * kWarps;
+    const int at = min(warp + i * kWarps, ROWS - 1);  // the last row may come twice
+    const unsigned row = row0 + at;
     const unsigned tok = row / p.group, head = row - tok * p.group;
     const T* src = static_cast<const T*>(p.q) + (q0 + tok) * p.ldq + (kvh * p.group + head) * D;
 #pragma unroll
@@ -141,7 +162,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
       note_status(p.status, PIQ_ERR_INVALID_ARG, b);
       pg = 0;
     }
-    s_base[i] = (static_cast<int64_t>(pg) * p.kv_heads + kvh) * p.block * D;
+    s_page[i] = pg * p.kv_heads + kvh;
     s_ks[i] = ks;
     s_vs[i] = vs;
   }
@@ -158,7 +179,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
     if (__any_sync(0xffffffffu, nan)) amax = __uint_as_float(0x7FC00000u);
     float mul, sum = 0.0f;
     const float undo = row_exponent<T>(amax, mul);
-    const int at = warp + i * kWarps;
+    const int at = min(warp + i * kWarps, ROWS - 1);
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) {
       const __half h = __float2half_rn(undo == undo ? qv[i][j] * mul : 0.0f);
@@ -174,37 +195,48 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
   }
   __syncthreads();
 
-  // ------------------------------------------------------------- the keys, 16 a step
+  // ------------------------------------------------------------- the keys, 32 a step
+  // Two tiles of 16 keys: two independent chains of products, and the votes and
+  // address work once for both.
   const int ntiles = (nkeys + 15) / 16;
+  const int steps = (nkeys + 31) / 32;
   const int tshift = shift - 4;  // log2 of the tiles of a page
   const int in_page = (1 << tshift) - 1;
-  const int8_t* const kbase = p.kc + r * D + 16 * c;
-  const int8_t* const vbase = p.vc + 2 * c * D + r * (D / 8);
-  // stage i of the ring: the key pieces (16 bytes a lane, 512 apart), then the values'
   uint8_t* const mine = ring + warp * kRing;
-  auto fetch = [&](int tile, int stage) {
-    const int64_t base = s_base[tile >> tshift] + (tile & in_page) * (16 * D);
-    const int8_t *ka = kbase + base, *va = vbase + base;
-    uint8_t* to = mine + stage * STAGE + 16 * lane;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int j = 0; j < KV; ++j) cp_async16(to + (h * KV + j) * 512, ka + 8 * h * D + 64 * j);
-    to = mine + stage * STAGE + 16 * D + (D / 8) * lane;
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const int8_t* a = va + ((h & 1) + 8 * (h >> 1)) * D;
-      if constexpr (D == 128)
-        cp_async16(to + h * 512, a);
-      else
-        cp_async8(to + h * 256, a);
+  auto fetch = [&](int step, int stage) {  // lane 0
+    uint8_t* to = mine + stage * STAGE;
+    const int tile = 2 * step;
+    if (tshift > 0) {  // 32 keys of one page (those past the last one lie in it too)
+      mbar_arrive_expect_tx(&full[warp][stage], STAGE);
+      const int z = s_page[tile >> tshift], y = (tile & in_page) * 16;
+      tma_load_3d(to, &tm_k, &full[warp][stage], 0, y, z);
+      tma_load_3d(to + 32 * D, &tm_v, &full[warp][stage], 0, y, z);
+    } else {           // pages of 16
+      const int two = tile + 1 < ntiles ? 2 : 1;
+      mbar_arrive_expect_tx(&full[warp][stage], two * (STAGE / 2));
+      for (int u = 0; u < two; ++u) {
+        tma_load_3d(to + u * (16 * D), &tm_k, &full[warp][stage], 0, 0, s_page[tile + u]);
+        tma_load_3d(to + 32 * D + u * (16 * D), &tm_v, &full[warp][stage], 0, 0, s_page[tile + u]);
+      }
     }
   };
+  if (lane == 0) {
 #pragma unroll
-  for (int i = 0; i < STAGES - 1; ++i) {
-    if (warp + i * kWarps < ntiles) fetch(warp + i * kWarps, i);
-    cp_async_commit();
+    for (int i = 0; i < STAGES; ++i)
+      if (warp + i * kWarps < steps) fetch(warp + i * kWarps, i);
   }
+  // where this lane's pieces lie in a swizzled tile of 16 tokens
+  const int tk = token_of<D>(r);
+  const int k_at = D == 128 ? tk * 128 + ((c ^ tk) << 4) : tk * 64 + ((c ^ (tk >> 1)) << 4);
+  const int eighth = D == 128 ? (r & 1) * 4 + (r >> 1) : r;  // dimensions eighth D / 8 ..
+  int v_at[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int tv = token_of<D>(2 * c + h);
+    v_at[h] = 32 * D + (D == 128 ? tv * 128 + ((eighth ^ tv) << 4)
+                                 : tv * 64 + (((r >> 1) ^ (tv >> 1)) << 4) + (r & 1) * 8);
+  }
+
   // -------------------------------------------------------------- fragments of q
   uint32_t qf[NT][KS][2];
   float rs[NT][2], qs[NT][2];
@@ -244,67 +276,69 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
   }
 
   int stage = 0;
-#pragma unroll 1
-  for (int tile = warp; tile < ntiles; tile += kWarps) {
-    const int key0 = 16 * tile;
-    cp_async_wait<STAGES - 2>();
-    {
-      const int next = tile + (STAGES - 1) * kWarps;
-      if (next < ntiles) fetch(next, stage == 0 ? STAGES - 1 : stage - 1);
-      cp_async_commit();
+  uint32_t phase = 0;
+  bool ok = true;
+  // One step; MASK: some row does not see all of its keys.  Two forms, because the
+  // compiler would turn a branch around the masks into selects on every step.
+  auto process = [&](int step, auto mask_c) {
+    constexpr bool MASK = decltype(mask_c)::value;
+    const uint8_t* const at = mine + stage * STAGE;
+    const int key0 = 32 * step;
+    float s[2][NT][4] = {}, kscale[2], vscale[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      // a second tile behind the last keys is all masked; it borrows a page's scales
+      const int page = (MASK ? min(2 * step + u, ntiles - 1) : 2 * step + u) >> tshift;
+      kscale[u] = s_ks[page];
+      vscale[u] = s_vs[page];
     }
-    const uint8_t* const kat = mine + stage * STAGE + 16 * lane;
-    const uint8_t* const vat = mine + stage * STAGE + 16 * D + (D / 8) * lane;
-    stage = stage == STAGES - 1 ? 0 : stage + 1;
-    uint4 kr[2][KV];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int j = 0; j < KV; ++j)
 #pragma unroll
-      for (int j = 0; j < KV; ++j)
-        kr[h][j] = *reinterpret_cast<const uint4*>(kat + (h * KV + j) * 512);
-    float s[NT][4] = {}, s2[NT][4] = {};  // two chains of products
+      for (int u = 0; u < 2; ++u) {
+        const uint8_t* a = at + u * (16 * D) + (k_at ^ (64 * j));
+        const uint4 w0 = *reinterpret_cast<const uint4*>(a);
+        const uint4 w1 = *reinterpret_cast<const uint4*>(a + 8 * D);
+        const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const uint4 w0 = kr[0][ks / 4], w1 = kr[1][ks / 4];
-      const uint32_t x0 = ks % 4 == 0 ? w0.x : ks % 4 == 1 ? w0.y : ks % 4 == 2 ? w0.z : w0.w;
-      const uint32_t x1 = ks % 4 == 0 ? w1.x : ks % 4 == 1 ? w1.y : ks % 4 == 2 ? w1.z : w1.w;
-      uint32_t a0, a1, a2, a3;
-      biased_halves_of(x0, a0, a2);
-      biased_halves_of(x1, a1, a3);
+        for (int w = 0; w < 4; ++w) {
+          uint32_t a0, a1, a2, a3;
+          biased_halves_of(x0[w], a0, a2);
+          biased_halves_of(x1[w], a1, a3);
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-        mma_f16(ks & 1 ? s2[t] : s[t], a0, a1, a2, a3, qf[t][ks][0], qf[t][ks][1]);
-    }
-    const float kscale = s_ks[tile >> tshift], vscale = s_vs[tile >> tshift];
+          for (int t = 0; t < NT; ++t)
+            mma_f16(s[u][t], a0, a1, a2, a3, qf[t][4 * j + w][0], qf[t][4 * j + w][1]);
+        }
+      }
 
     // scores in log2 units
-    bool over = false;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const float f0 = rs[t][0] * kscale, f1 = rs[t][1] * kscale;
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        s[t][e] = fmaf(s[t][e] + s2[t][e], 0x1p24f, qs[t][e & 1]) * (e & 1 ? f1 : f0);
-    }
-    const bool masked = key0 < all_lo || key0 + 16 > all_hi;
-    if (masked) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < NT; ++t) {
+        const float f0 = rs[t][0] * kscale[u], f1 = rs[t][1] * kscale[u];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int j = key0 + r + 8 * (e >> 1), h = hi[t][e & 1];
-          const bool see = j < h && (window == 0 || j >= h - window);
-          if (!see) s[t][e] = __uint_as_float(0xFF800000u);
+          s[u][t][e] = fmaf(s[u][t][e], 0x1p24f, qs[t][e & 1]) * (e & 1 ? f1 : f0);
+          if (MASK) {
+            const int j = key0 + 16 * u + tk + 8 * (e >> 1), h = hi[t][e & 1];
+            const bool see = j < h && (window == 0 || j >= h - window);
+            if (!see) s[u][t][e] = __uint_as_float(0xFF800000u);
+          }
         }
-    }
+      }
+    bool over = fmaxf(vscale[0], vscale[1]) > vmax;
+    float top[NT][2];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      over |= fmaxf(s[t][0], s[t][2]) > m[t][0] + kSlack;
-      over |= fmaxf(s[t][1], s[t][3]) > m[t][1] + kSlack;
-    }
-    if (__any_sync(0xffffffffu, over || vscale > vmax)) {
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        top[t][e] = fmaxf(fmaxf(s[0][t][e], s[0][t][e + 2]), fmaxf(s[1][t][e], s[1][t][e + 2]));
+        over |= top[t][e] > m[t][e] + kSlack;
+      }
+    if (__any_sync(0xffffffffu, over)) {
       // the maximum (or the largest value scale) moves: what was summed is rescaled
-      const float fresh = fmaxf(vscale, vmax);
+      const float fresh = fmaxf(fmaxf(vscale[0], vscale[1]), vmax);
       const float fv = vmax > 0.0f ? vmax / fresh : 0.0f;
       vmax = fresh;
 #pragma unroll
@@ -312,7 +346,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
         float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float x = fmaxf(s[t][e], s[t][e + 2]);
+          float x = top[t][e];
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
@@ -333,57 +367,79 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
     }
     // probabilities; those of the values carry the block's scale (NaN scales stay NaN,
     // but only where a key is seen)
-    const float vf = vmax > 0.0f ? __fdividef(kPScale * vscale, vmax) : (vscale == vscale ? 0.0f : vscale);
-    uint32_t pb[NT][2];
+    uint32_t pb[2][NT][2];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int u = 0; u < 2; ++u) {
+      const float vf = vmax > 0.0f ? __fdividef(kPScale * vscale[u], vmax)
+                                   : (vscale[u] == vscale[u] ? 0.0f : vscale[u]);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float p0 = exp2_fast(s[t][2 * h] - m[t][0]);
-        const float p1 = exp2_fast(s[t][2 * h + 1] - m[t][1]);
-        l[t][0] += p0;
-        l[t][1] += p1;
-        float y0 = p0 * vf, y1 = p1 * vf;
-        if (masked) {
-          y0 = p0 == 0.0f ? 0.0f : y0;
-          y1 = p1 == 0.0f ? 0.0f : y1;
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float p0 = exp2_fast(s[u][t][2 * h] - m[t][0]);
+          const float p1 = exp2_fast(s[u][t][2 * h + 1] - m[t][1]);
+          l[t][0] += p0;
+          l[t][1] += p1;
+          float y0 = p0 * vf, y1 = p1 * vf;
+          if (MASK) {
+            y0 = p0 == 0.0f ? 0.0f : y0;
+            y1 = p1 == 0.0f ? 0.0f : y1;
+          }
+          const __half2 ph = __floats2half2_rn(y0, y1);
+          pb[u][t][h] = transpose8x8(*reinterpret_cast<const uint32_t*>(&ph));
         }
-        const __half2 ph = __floats2half2_rn(y0, y1);
-        pb[t][h] = transpose8x8(*reinterpret_cast<const uint32_t*>(&ph));
+    }
+    // keys past the end of the sequence: their codes are whatever lies there, times 0
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t vr[4][D / 32];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const uint8_t* a = at + u * (16 * D) + v_at[h & 1] + (h >> 1) * (8 * D);
+        if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(a);
+          vr[h][0] = x.x;
+          vr[h][1] = x.y;
+          vr[h][2] = x.z;
+          vr[h][3] = x.w;
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(a);
+          vr[h][0] = x.x;
+          vr[h][1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w) {
+        // four dimensions of tokens k = 2c, 2c + 1 and 2c + 8, 2c + 9
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t sel = half == 0 ? 0x5410u : 0x7632u;  // d0 d1 | d2 d3 of both tokens
+          uint32_t a0, a1, a2, a3;
+          halves_of(__byte_perm(vr[0][w], vr[1][w], sel), a0, a1);
+          halves_of(__byte_perm(vr[2][w], vr[3][w], sel), a2, a3);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            mma_f16(o[t][2 * w + half], a0, a1, a2, a3, pb[u][t][0], pb[u][t][1]);
+        }
       }
     }
-    uint32_t vr[4][D / 32];
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      if constexpr (D == 128) {
-        const uint4 x = *reinterpret_cast<const uint4*>(vat + h * 512);
-        vr[h][0] = x.x;
-        vr[h][1] = x.y;
-        vr[h][2] = x.z;
-        vr[h][3] = x.w;
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(vat + h * 256);
-        vr[h][0] = x.x;
-        vr[h][1] = x.y;
-      }
-    }
-    // keys past the end of the page's tokens: their codes are whatever lies there, times 0
-#pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
-      // four dimensions of tokens (2c, 2c + 1) and (2c + 8, 2c + 9)
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t sel = half == 0 ? 0x5410u : 0x7632u;  // d0 d1 | d2 d3 of both tokens
-        uint32_t a0, a1, a2, a3;
-        halves_of(__byte_perm(vr[0][w], vr[1][w], sel), a0, a1);
-        halves_of(__byte_perm(vr[2][w], vr[3][w], sel), a2, a3);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) mma_f16(o[t][2 * w + half], a0, a1, a2, a3, pb[t][0], pb[t][1]);
-      }
+  };
+#pragma unroll 1
+  for (int step = warp; step < steps; step += kWarps) {
+    if (!(ok = wait_warp(&full[warp][stage], phase, p.status, 91))) break;
+    if (32 * step < all_lo || 32 * step + 32 > all_hi)
+      process(step, std::true_type());
+    else
+      process(step, std::false_type());
+    __syncwarp();  // every lane has read the stage
+    if (lane == 0 && step + STAGES * kWarps < steps) fetch(step + STAGES * kWarps, stage);
+    if (++stage == STAGES) {
+      stage = 0;
+      phase ^= 1u;
     }
   }
+
   // --------------------------------------------------------------- join the warps
-  cp_async_wait<0>();
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -415,9 +471,9 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
         for (int j = 0; j < KS; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            // tile j holds dimensions r D / 8 + 2 j (rows 0 - 7) and + 2 j + 1 (rows 8 - 15)
+            // tile j holds dimensions 2 j (rows 0 - 7) and 2 j + 1 (rows 8 - 15) of an eighth
             float* at = &s_o[warp % (kWarps / 2)][8 * t + 2 * c + (e & 1)]
-                            [r * (D / 8) + 2 * j + (e >> 1)];
+                            [eighth * (D / 8) + 2 * j + (e >> 1)];
             const float x = o[t][j][e] * f[t][e & 1];
             *at = pass == 0 ? x : *at + x;
           }
@@ -593,6 +649,23 @@ AttnWs attn_ws(const AttnPlan& a, int64_t tokens, int heads, int head_dim) {
   return w;
 }
 
+// The codes as [pages kv_heads][block][D], in boxes of 32 tokens (16 where a page has
+// no more), swizzled over a token's bytes.
+template <int D>
+bool page_map(CUtensorMap* map, const int8_t* codes, const Kv8Attn& p) {
+  const EncodeTiledFn fn = tensor_map_encoder();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(p.block),
+                              static_cast<cuuint64_t>(p.pages) * p.kv_heads};
+  const cuuint64_t strides[2] = {D, static_cast<cuuint64_t>(D) * p.block};
+  const cuuint32_t box[3] = {D, static_cast<cuuint32_t>(std::min(p.block, 32)), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t*>(codes), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T, int D>
 int launch_join(const Kv8Attn& p, cudaStream_t stream) {
   note_launch();
@@ -609,9 +682,11 @@ int launch_attention(const Kv8Attn& p, const AttnPlan& a, cudaStream_t stream) {
     if (rc != PIQ_OK) return rc;
     return a.chunks == 1 ? PIQ_OK : launch_join<T, D>(p, stream);
   }
-  void (*kern)(Kv8Attn) = a.nt == 1 ? kv8_chunk_kernel<T, D, 1> : kv8_chunk_kernel<T, D, 2>;
+  void (*kern)(CUtensorMap, CUtensorMap, Kv8Attn) = a.nt == 1 ? kv8_chunk_kernel<T, D, 1> : kv8_chunk_kernel<T, D, 2>;
   const unsigned gx = static_cast<unsigned>(a.row_groups * p.kv_heads);
-  constexpr int smem = kWarps * kRing;
+  constexpr int smem = kWarps * kRing + 1024;
+  CUtensorMap mk, mv;
+  if (!page_map<D>(&mk, p.kc, p) || !page_map<D>(&mv, p.vc, p)) return PIQ_ERR_INVALID_ARG;
   static std::atomic<bool> set[2][64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return PIQ_ERR_CUDA;
@@ -622,7 +697,7 @@ int launch_attention(const Kv8Attn& p, const AttnPlan& a, cudaStream_t stream) {
     if (done != nullptr) done->store(true, std::memory_order_release);
   }
   note_launch();
-  if (launch_pdl(kern, dim3(gx, a.chunks, p.batch), dim3(32 * kWarps), smem, stream, p) !=
+  if (launch_pdl(kern, dim3(gx, a.chunks, p.batch), dim3(32 * kWarps), smem, stream, mk, mv, p) !=
       cudaSuccess)
     return PIQ_ERR_CUDA;
   return a.chunks == 1 ? PIQ_OK : launch_join<T, D>(p, stream);

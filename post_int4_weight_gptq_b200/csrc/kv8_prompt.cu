@@ -34,24 +34,6 @@ constexpr int KT = 128;      // keys a tile
 constexpr int kThreads = 16 * 32;
 constexpr int kGran = KT / 16;  // 16-key granules: never across a page
 
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int32_t* status,
-                                         int where) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  for (;;) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (global_timer_ns() - t0 > kWaitLimitNs) {
-      note_status(status, PIQ_ERR_TIMEOUT, where);
-      return false;
-    }
-  }
-}
-// The same for a whole warp, which goes on or gives up together.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int32_t* status,
-                                          int where) {
-  return __all_sync(0xffffffffu, wait_bar(bar, parity, status, where));
-}
-
 // fp16 A and B, fp32 D; B optionally MN-major.
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool b_mn) {
   return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |

@@ -1,6 +1,7 @@
 // Shared pieces of the 8-bit serving entries (int8.cu, kv8.cu, kv8_attn.cu).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -22,6 +23,33 @@ Int8Plan plan_int8(int64_t tokens, int64_t out, int64_t in, int sms);
 int launch_int8_gemm(const int8_t* qx, int64_t ldq, const float* sx, int64_t tokens, int64_t in,
                      const int8_t* W, int64_t out, int64_t ldw, const float* sw, const float* bias,
                      void* Y, int dtype, int64_t ldy, int32_t* status, cudaStream_t stream);
+
+// cuTensorMapEncodeTiled of the loaded driver, nullptr if it has none.
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn tensor_map_encoder();
+
+// A bounded wait (mbar_wait) that reports to the caller's status words.
+__device__ __forceinline__ void note_status(int32_t* status, int code, int detail);
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int32_t* status,
+                                         int where) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      note_status(status, PIQ_ERR_TIMEOUT, where);
+      return false;
+    }
+  }
+}
+// The same for a whole warp, which goes on or gives up together.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int32_t* status,
+                                          int where) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, status, where));
+}
 
 inline bool ptr_aligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
