@@ -97,22 +97,22 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
   constexpr int KV = D / 64;   // 16-byte loads of a key a lane; value loads are 4 of D / 8 bytes
   constexpr int STAGE = 64 * D;            // bytes of 32 keys, then their 32 values
   constexpr int STAGES = kRing / STAGE;
-  constexpr int OLD = D + 4;   // row stride of the joined output in shared memory
   __shared__ int s_page[kMaxPages];  // page kv_heads + head
   __shared__ float s_ks[kMaxPages], s_vs[kMaxPages];
   __shared__ __align__(16) __half s_q[ROWS][D];
   __shared__ float s_rs[ROWS], s_qs[ROWS];
-  __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
+  __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS], s_v[kWarps];
   __shared__ uint64_t full[kWarps][STAGES];
   extern __shared__ uint8_t ring_raw[];  // the warps' rings, then the join's buffer
   uint8_t* const ring = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(ring_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  float(*s_o)[ROWS][OLD] = reinterpret_cast<float(*)[ROWS][OLD]>(ring);
-  static_assert(sizeof(float) * (kWarps / 2) * ROWS * OLD <= kWarps * kRing, "join buffer");
+  float* const s_o = reinterpret_cast<float*>(ring);
+  static_assert(sizeof(float) * NT * KS * 4 * 32 <= kRing, "join buffer");
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (lane < STAGES) mbar_init(&full[warp][lane], 1);
   fence_mbar_init();
+  __syncwarp();
   pdl_launch_dependents();
   pdl_wait();
   const int r = lane >> 2, c = lane & 3;
@@ -150,8 +150,45 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
     for (int j = 0; j < D / 32; ++j)
       qv[i][j] = row < static_cast<unsigned>(rows) ? to_float(__ldg(src + 32 * j + lane)) : 0.0f;
   }
+  // ------------------------------------------------------------- the keys, 32 a step
+  // Two tiles of 16 keys: two independent chains of products, and the votes and
+  // address work once for both.
+  const int ntiles = (nkeys + 15) / 16;
+  const int steps = (nkeys + 31) / 32;
+  const int tshift = shift - 4;  // log2 of the tiles of a page
+  const int in_page = (1 << tshift) - 1;
+  uint8_t* const mine = ring + warp * kRing;
+  auto fetch = [&](int step, int stage, auto page_of) {  // lane 0; page_of(i): place of page i
+    uint8_t* to = mine + stage * STAGE;
+    const int tile = 2 * step;
+    if (tshift > 0) {  // 32 keys of one page (those past the last one lie in it too)
+      mbar_arrive_expect_tx(&full[warp][stage], STAGE);
+      const int z = page_of(tile >> tshift), y = (tile & in_page) * 16;
+      tma_load_3d(to, &tm_k, &full[warp][stage], 0, y, z);
+      tma_load_3d(to + 32 * D, &tm_v, &full[warp][stage], 0, y, z);
+    } else {           // pages of 16
+      const int two = tile + 1 < ntiles ? 2 : 1;
+      mbar_arrive_expect_tx(&full[warp][stage], two * (STAGE / 2));
+      for (int u = 0; u < two; ++u) {
+        const int z = page_of(tile + u);
+        tma_load_3d(to + u * (16 * D), &tm_k, &full[warp][stage], 0, 0, z);
+        tma_load_3d(to + 32 * D + u * (16 * D), &tm_v, &full[warp][stage], 0, 0, z);
+      }
+    }
+  };
+  // The first stages go out before anything else is known but the pages.
   const int npages = (nkeys + p.block - 1) >> shift;
   const int32_t* table = p.table + b * p.ldt + (k0 >> shift);
+  if (lane == 0) {
+    auto direct = [&](int i) {
+      const int pg = __ldg(table + i);
+      return (pg >= 0 && pg < p.pages ? pg : 0) * p.kv_heads + kvh;
+    };
+#pragma unroll 1
+    for (int i = 0; i < STAGES; ++i)
+      if (warp + i * kWarps < steps) fetch(warp + i * kWarps, i, direct);
+  }
+  __syncwarp();
   for (int i = threadIdx.x; i < npages; i += blockDim.x) {
     int pg = __ldg(table + i);
     float ks = __uint_as_float(0x7FC00000u), vs = ks;
@@ -195,36 +232,6 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
   }
   __syncthreads();
 
-  // ------------------------------------------------------------- the keys, 32 a step
-  // Two tiles of 16 keys: two independent chains of products, and the votes and
-  // address work once for both.
-  const int ntiles = (nkeys + 15) / 16;
-  const int steps = (nkeys + 31) / 32;
-  const int tshift = shift - 4;  // log2 of the tiles of a page
-  const int in_page = (1 << tshift) - 1;
-  uint8_t* const mine = ring + warp * kRing;
-  auto fetch = [&](int step, int stage) {  // lane 0
-    uint8_t* to = mine + stage * STAGE;
-    const int tile = 2 * step;
-    if (tshift > 0) {  // 32 keys of one page (those past the last one lie in it too)
-      mbar_arrive_expect_tx(&full[warp][stage], STAGE);
-      const int z = s_page[tile >> tshift], y = (tile & in_page) * 16;
-      tma_load_3d(to, &tm_k, &full[warp][stage], 0, y, z);
-      tma_load_3d(to + 32 * D, &tm_v, &full[warp][stage], 0, y, z);
-    } else {           // pages of 16
-      const int two = tile + 1 < ntiles ? 2 : 1;
-      mbar_arrive_expect_tx(&full[warp][stage], two * (STAGE / 2));
-      for (int u = 0; u < two; ++u) {
-        tma_load_3d(to + u * (16 * D), &tm_k, &full[warp][stage], 0, 0, s_page[tile + u]);
-        tma_load_3d(to + 32 * D + u * (16 * D), &tm_v, &full[warp][stage], 0, 0, s_page[tile + u]);
-      }
-    }
-  };
-  if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < STAGES; ++i)
-      if (warp + i * kWarps < steps) fetch(warp + i * kWarps, i);
-  }
   // where this lane's pieces lie in a swizzled tile of 16 tokens
   const int tk = token_of<D>(r);
   const int k_at = D == 128 ? tk * 128 + ((c ^ tk) << 4) : tk * 64 + ((c ^ (tk >> 1)) << 4);
@@ -432,7 +439,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
     else
       process(step, std::false_type());
     __syncwarp();  // every lane has read the stage
-    if (lane == 0 && step + STAGES * kWarps < steps) fetch(step + STAGES * kWarps, stage);
+    if (lane == 0 && step + STAGES * kWarps < steps) fetch(step + STAGES * kWarps, stage, [&](int i) { return s_page[i]; });
     if (++stage == STAGES) {
       stage = 0;
       phase ^= 1u;
@@ -440,8 +447,18 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
   }
 
   // --------------------------------------------------------------- join the warps
+  // Every warp leaves its sums as they lie in its lanes; behind one barrier a thread
+  // takes 8 neighbouring dimensions of a row (a lane's, half an eighth or a whole
+  // one) and adds the warps' with their factors.
+  __syncthreads();  // all rings are read
+  float* const mine_o = s_o + warp * (NT * KS * 4 * 32) + lane;
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int j = 0; j < KS; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        mine_o[((t * 2 + (e & 1)) * (D / 8) + 2 * j + (e >> 1)) * 32] = o[t][j][e];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 4);
@@ -452,59 +469,49 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
         s_l[warp][8 * t + 2 * c + e] = l[t][e];
       }
     }
-  __syncthreads();
-  float f[NT][2];
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float top = kLow;
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][8 * t + 2 * c + e]);
-      f[t][e] = exp2_fast(m[t][e] - top) * (vmax / kPScale);
-    }
-  // halves of the warps in turn, each adding into a buffer of its own
-  for (int pass = 0; pass < 2; ++pass) {
-    if (warp / (kWarps / 2) == pass) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int j = 0; j < KS; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            // tile j holds dimensions 2 j (rows 0 - 7) and 2 j + 1 (rows 8 - 15) of an eighth
-            float* at = &s_o[warp % (kWarps / 2)][8 * t + 2 * c + (e & 1)]
-                            [eighth * (D / 8) + 2 * j + (e >> 1)];
-            const float x = o[t][j][e] * f[t][e & 1];
-            *at = pass == 0 ? x : *at + x;
-          }
-    }
-    __syncthreads();
   }
-  for (int i = warp; i < ROWS; i += kWarps) {
-    const int row = row0 + i;
-    if (row >= rows) break;
-    float top = kLow, sum = 0.0f;
+  if (lane == 0) s_v[warp] = vmax / kPScale;
+  __syncthreads();
+  constexpr int PARTS = D / 64;  // threads for a lane's dimensions of one row
+  for (int i = threadIdx.x; i < NT * 64 * PARTS; i += 32 * kWarps) {
+    const int src = i & 31, te = (i >> 5) % (2 * NT), piece = i / (64 * NT);
+    const int at = 8 * (te >> 1) + 2 * (src & 3) + (te & 1);  // row of the group
+    const int row = row0 + at;
+    if (row >= rows) continue;
+    float top = kLow, sum = 0.0f, f[kWarps], x[8] = {};
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][i]);
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][at]);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += s_l[w][i] * exp2_fast(s_m[w][i] - top);
+    for (int w = 0; w < kWarps; ++w) {
+      f[w] = exp2_fast(s_m[w][at] - top);
+      sum += s_l[w][at] * f[w];
+      f[w] *= s_v[w];
+    }
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+      for (int d = 0; d < 8; ++d)
+        x[d] = fmaf(s_o[w * (NT * KS * 4 * 32) + (te * (D / 8) + 8 * piece + d) * 32 + src], f[w],
+                    x[d]);
+    const int sr = src >> 2;
+    const int dim = (D == 128 ? ((sr & 1) * 4 + (sr >> 1)) * 16 : sr * 8) + 8 * piece;
     const unsigned tok = static_cast<unsigned>(row) / p.group;
     const int64_t t = q0 + tok;
     const int head = kvh * p.group + static_cast<int>(row - tok * p.group);
-    const float norm = single ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
     const int64_t slot = (static_cast<int64_t>(part) * p.tokens + t) * p.heads + head;
+    if (single) {
+      const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
+      uint4 v;
+      T* w = reinterpret_cast<T*>(&v);
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
-      float x = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps / 2; ++w) x += s_o[w][i][32 * j + lane];
-      x *= norm;
-      if (single)
-        out[t * p.ldo + head * D + 32 * j + lane] = from_float<T>(x);
-      else
-        p.part_o[slot * D + 32 * j + lane] = x;
+      for (int d = 0; d < 8; ++d) w[d] = from_float<T>(x[d] * norm);
+      *reinterpret_cast<uint4*>(out + t * p.ldo + head * D + dim) = v;
+    } else {
+      float4* to = reinterpret_cast<float4*>(p.part_o + slot * D + dim);
+      to[0] = make_float4(x[0], x[1], x[2], x[3]);
+      to[1] = make_float4(x[4], x[5], x[6], x[7]);
     }
-    if (lane == 0) {
+    if (sr == 0 && piece == 0) {
       if (!single)
         p.part_ml[slot] = make_float2(top, sum);
       else if (p.lse != nullptr)
@@ -587,10 +594,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv8_join_kernel(Kv8Attn p) {
         total == 0.0f ? __uint_as_float(0xFF800000u) : (top + log2f(total)) * kLn2;
 }
 
-// Keys a chunk: enough CTAs for two waves of two a multiprocessor, but no
-// chunk so short that joining it costs more than it spreads.
-constexpr int64_t kMinChunk = 256, kMaxChunk = 4096, kMinPromptChunk = 512;
-constexpr int64_t kManyRows = 32;  // rows a kv head above which the tensor-memory kernel runs
+// Keys a chunk: one wave of two CTAs a multiprocessor where the sequences and heads
+// alone do not fill it, but no chunk so short that starting and joining it costs
+// more than it spreads; where they do, chunks that even out ragged lengths.
+constexpr int64_t kMinChunk = 256, kManyCtasChunk = 2048, kMaxChunk = 4096;
+constexpr int64_t kMinPromptChunk = 512;
+constexpr int64_t kManyRows = 16;  // rows a kv head above which the tensor-memory kernel runs
 
 struct AttnPlan {
   bool prompt;       // kv8_prompt.cu
@@ -622,8 +631,8 @@ AttnPlan plan_attention(int64_t tokens, int heads, int kv_heads, int64_t batch, 
     return a;
   }
   const int64_t ctas = a.row_groups * kv_heads * batch;
-  const int64_t want = std::max<int64_t>(1, 2 * 148 / ctas);
-  a.chunk = ceil_div(ceil_div(span, want), 128) * 128;
+  const int64_t want = 2 * 148 / ctas;
+  a.chunk = want > 1 ? ceil_div(ceil_div(span, want), 128) * 128 : kManyCtasChunk;
   a.chunk = std::min(std::max(a.chunk, kMinChunk), kMaxChunk);
   a.chunks = static_cast<int>(ceil_div(span, a.chunk));
   return a;
