@@ -20,7 +20,7 @@ from __future__ import annotations
 
 import collections
 import ctypes
-import functools
+import importlib.util
 import os
 
 import torch
@@ -516,78 +516,31 @@ def upper_factor_noalloc(H, damp=0.01, perm=None, stream=None):
 
 
 # ------------------------------------------------------------- 8-bit serving layer
-# These calls sit in a decoding loop, where the host's time is the step's: their
-# checks are one expression each on the way that holds, and say what is wrong only
-# when something is.
-_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-_HALF = {torch.bfloat16: 0, torch.float16: 1}
-_INT8 = {torch.int8: 0}
-_INT32 = {torch.int32: 0}
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+# These calls sit in a decoding loop, where the host's time is the step's: they go
+# through lib/piq_serve.so (csrc/serve_binding.cpp), which checks the tensors, makes
+# the outputs and calls the C ABI; ctypes took 10 to 20 us a call for that.
+SERVE_PATH = os.path.join(_HERE, "lib", "piq_serve.so")
+_serve = None
 
 
-def _rows_of(t, name, ndim, dtypes):
-    """Checks a tensor of rows: on the GPU, of a type the entry takes, every
-    row (all but the first dimension) contiguous.  The row stride in elements."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} has an unsupported dtype: {t.dtype}")
-    shape, stride = t.shape, t.stride()
-    if len(shape) != ndim:
-        raise ValueError(f"{name} must have {ndim} dimensions, got {t.ndim}")
-    want = 1
-    for i in range(ndim - 1, 0, -1):
-        if stride[i] != want and shape[i] > 1 and shape[0]:
-            raise ValueError(f"the rows of {name} must be contiguous")
-        want *= shape[i]
-    return stride[0] if shape[0] > 1 else max(stride[0], want)
+def _serving():
+    """The binding of the 8-bit calls (raises if it has not been built)."""
+    global _serve
+    if _serve is None:
+        load_library()
+        if not os.path.exists(SERVE_PATH):
+            raise RuntimeError(f"{SERVE_PATH} is missing: build it with "
+                               "`python -m post_int4_weight_gptq_b200.build`")
+        spec = importlib.util.spec_from_file_location("piq_serve", SERVE_PATH)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.set_check(_check)
+        _serve = mod
+    return _serve
 
 
-def _flat(t, dtype, name, shape, dev):
-    """Checks a contiguous tensor of a given type, shape and device."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous of shape {tuple(shape)}, got "
-                         f"{tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not {dev}")
-
-
-def _same_device(dev, *tensors):
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on different devices: {t.device} and {dev}")
-
-
-def _on(dev, stream, call, *args):
-    """call(raw stream, ...) with the tensors' device current; with a stream of
-    its own, what the call allocates comes from that stream's memory too."""
-    if stream is None and torch.cuda.current_device() == dev.index:
-        return call(_raw_stream(dev.index), *args)
-    with torch.cuda.device(dev):
-        with torch.cuda.stream(stream or torch.cuda.current_stream(dev)):
-            return call(_raw_stream(dev.index), *args)
-
-
-def _status_ptr(status, dev):
-    if status is None:
-        return None
-    _flat(status, torch.int32, "status", (2,), dev)
-    return status.data_ptr()
-
-
-def _work(nbytes, dev, workspace):
-    """The caller's workspace if it is large enough, else a new one."""
-    if workspace is None or workspace.numel() < nbytes:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _flat(workspace, torch.uint8, "workspace", workspace.shape, dev)
-    return workspace
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def new_status(device=None):
@@ -608,22 +561,9 @@ def int8_quantize_rows(X, stream=None):
     """(codes, scales): every row of X [rows, cols] (bf16, fp16 or fp32) as int8
     codes with one fp32 scale; the tokens of an activation or the channels of a
     weight.  The row stride of the codes is padded to 16."""
-    ldx = _rows_of(X, "X", 2, _DTYPES)
-    return _on(X.device, stream, _int8_quantize_rows, X, ldx)
+    return (_serve or _serving()).int8_quantize_rows(X, _handle(stream))
 
 
-def _int8_quantize_rows(s, X, ldx):
-    rows, cols = X.shape
-    ldc = (cols + 15) // 16 * 16
-    codes = X.new_empty((rows, ldc), dtype=torch.int8)
-    scales = X.new_empty(rows, dtype=torch.float32)
-    _check(load_library().piq_int8_quantize_rows(X.data_ptr(), _DTYPES[X.dtype], rows, cols, ldx,
-                                                 codes.data_ptr(), ldc, scales.data_ptr(), s),
-           "piq_int8_quantize_rows")
-    return (codes if ldc == cols else codes[:, :cols]), scales
-
-
-@functools.lru_cache(maxsize=4096)
 def int8_linear_workspace_bytes(tokens, out, inp) -> int:
     return _query(load_library().piq_int8_linear_workspace_bytes, tokens, out, inp)
 
@@ -633,34 +573,8 @@ def int8_linear(X, W, w_scale, bias=None, out=None, stream=None, workspace=None,
     are quantized inside the call, W [out, in] int8 and w_scale fp32 [out] are
     int8_quantize_rows of the weight (row stride a multiple of 16), bias is fp32
     [out].  The result has X's dtype."""
-    ldx = _rows_of(X, "X", 2, _DTYPES)
-    ldw = _rows_of(W, "W", 2, _INT8)
-    dev, n = X.device, W.shape[0]
-    if W.shape[1] != X.shape[1]:
-        raise ValueError("W and X disagree on the input dimension")
-    _flat(w_scale, torch.float32, "w_scale", (n,), dev)
-    if bias is not None:
-        _flat(bias, torch.float32, "bias", (n,), dev)
-    _same_device(dev, W, out)
-    return _on(dev, stream, _int8_linear, X, ldx, W, ldw, w_scale, bias, out, workspace, status)
-
-
-def _int8_linear(s, X, ldx, W, ldw, w_scale, bias, out, workspace, status):
-    tokens, inp = X.shape
-    n, dev = W.shape[0], X.device
-    if out is None:
-        out = X.new_empty((tokens, n))
-        ldy = n
-    else:
-        ldy = _rows_of(out, "out", 2, {X.dtype: 0})
-        if out.shape != (tokens, n):
-            raise ValueError(f"out must have shape {(tokens, n)}")
-    ws = _work(int8_linear_workspace_bytes(tokens, n, inp), dev, workspace)
-    _check(load_library().piq_int8_linear(
-        X.data_ptr(), _DTYPES[X.dtype], tokens, inp, ldx, W.data_ptr(), n, ldw,
-        w_scale.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(), ldy,
-        _status_ptr(status, dev), ws.data_ptr(), ws.numel(), s), "piq_int8_linear")
-    return out
+    return (_serve or _serving()).int8_linear(X, W, w_scale, bias, out, _handle(stream),
+                                              workspace, status)
 
 
 #: The 8-bit paged cache: codes int8 [pages, kv_heads, block, head_dim], scales
@@ -678,45 +592,13 @@ def kv8_cache(pages, kv_heads, head_dim, block=64, device=None):
                     torch.zeros(shape[:2], dtype=torch.float32, device=dev))
 
 
-def _kv8(cache, cu, lens, block_table):
-    """Checks a cache and its ragged batch: (device, cache arguments of the C
-    call, batch, table arguments)."""
-    k, v, ks, vs = cache
-    shape, dev = k.shape, k.device
-    if len(shape) != 4:
-        raise ValueError("cache.k must be [pages, kv_heads, block, head_dim]")
-    _flat(k, torch.int8, "cache.k", shape, dev)
-    _flat(v, torch.int8, "cache.v", shape, dev)
-    _flat(ks, torch.float32, "cache.k_scale", shape[:2], dev)
-    _flat(vs, torch.float32, "cache.v_scale", shape[:2], dev)
-    ldt = _rows_of(block_table, "block_table", 2, _INT32)
-    batch, width = block_table.shape
-    _flat(cu, torch.int32, "cu", (batch + 1,), dev)
-    _flat(lens, torch.int32, "lengths", (batch,), dev)
-    _same_device(dev, block_table)
-    return (dev, (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape[0], shape[1],
-                  shape[3], shape[2]), batch, (block_table.data_ptr(), width, ldt))
-
-
 def kv8_append(cache, k, v, cu, lens_before, block_table, stream=None, status=None):
     """Quantizes new keys and values k, v [tokens, kv_heads, head_dim] (bf16,
     fp16, fp32; token strides free, so slices of a fused projection do) into the
     cache behind the lens_before [batch] tokens each sequence has there; rows
     cu[b] .. cu[b + 1] - 1 are sequence b's."""
-    dev, c, batch, table = _kv8(cache, cu, lens_before, block_table)
-    ldk = _rows_of(k, "k", 3, _DTYPES)
-    ldv = _rows_of(v, "v", 3, {k.dtype: 0})
-    shape = k.shape
-    if shape != v.shape or shape[1] != c[5] or shape[2] != c[6]:
-        raise ValueError("k and v must be [tokens, kv_heads, head_dim] of the cache")
-    _same_device(dev, k, v)
-    _on(dev, stream, _kv8_append, k, v, ldk, ldv, cu, lens_before, batch, table, c, status)
-
-
-def _kv8_append(s, k, v, ldk, ldv, cu, lens, batch, table, c, status):
-    _check(load_library().piq_kv8_append(
-        k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], k.shape[0], ldk, ldv, cu.data_ptr(),
-        lens.data_ptr(), batch, *table, *c, _status_ptr(status, k.device), s), "piq_kv8_append")
+    (_serve or _serving()).kv8_append(*cache, k, v, cu, lens_before, block_table,
+                                      _handle(stream), status)
 
 
 def kv8_read(cache, cu, start, block_table, rows, dtype=torch.bfloat16, out=None, stream=None,
@@ -724,30 +606,11 @@ def kv8_read(cache, cu, start, block_table, rows, dtype=torch.bfloat16, out=None
     """(k, v) [rows, kv_heads, head_dim]: row cu[b] + i is sequence b's cached
     token start[b] + i.  Rows of no sequence are left as they are (`out`, a pair
     of tensors) or undefined."""
-    dev, c, batch, table = _kv8(cache, cu, start, block_table)
-    if dtype not in _DTYPES:
-        raise TypeError(f"unsupported dtype: {dtype}")
-    return _on(dev, stream, _kv8_read, cu, start, batch, table, c, rows, dtype, out, status)
+    k, v = out if out is not None else (None, None)
+    return (_serve or _serving()).kv8_read(*cache, cu, start, block_table, rows, dtype, k, v,
+                                           _handle(stream), status)
 
 
-def _kv8_read(s, cu, start, batch, table, c, rows, dtype, out, status):
-    shape, dev = (rows, c[5], c[6]), cu.device
-    if out is None:
-        k, v = cu.new_empty(shape, dtype=dtype), cu.new_empty(shape, dtype=dtype)
-        ldk = ldv = c[5] * c[6]
-    else:
-        k, v = out
-        ldk, ldv = _rows_of(k, "out", 3, {dtype: 0}), _rows_of(v, "out", 3, {dtype: 0})
-        if k.shape != shape or v.shape != shape:
-            raise ValueError(f"out must be two tensors of shape {shape}")
-        _same_device(dev, k, v)
-    _check(load_library().piq_kv8_read(
-        *c, cu.data_ptr(), start.data_ptr(), batch, *table, rows, k.data_ptr(), v.data_ptr(),
-        _DTYPES[dtype], ldk, ldv, _status_ptr(status, dev), s), "piq_kv8_read")
-    return k, v
-
-
-@functools.lru_cache(maxsize=4096)
 def kv8_attention_workspace_bytes(tokens, heads, kv_heads, head_dim, batch, max_new, max_len,
                                   window=0) -> int:
     return _query(load_library().piq_kv8_attention_workspace_bytes, tokens, heads, kv_heads,
@@ -762,32 +625,6 @@ def kv8_attention(cache, q, cu, lens, block_table, max_new, max_len, scale=None,
     rows and lens of every sequence; scale defaults to head_dim ** -0.5; window
     > 0 limits a query to the last `window` keys.  Returns out, or (out, lse)
     with lse fp32 [tokens, heads]."""
-    dev, c, batch, table = _kv8(cache, cu, lens, block_table)
-    ldq = _rows_of(q, "q", 3, _HALF)
-    if q.shape[2] != c[6]:
-        raise ValueError("q and the cache disagree on head_dim")
-    _same_device(dev, q, out)
-    return _on(dev, stream, _kv8_attention, q, ldq, cu, lens, batch, table, c, scale, window,
-               max_new, max_len, out, return_lse, workspace, status)
-
-
-def _kv8_attention(s, q, ldq, cu, lens, batch, table, c, scale, window, max_new, max_len, out,
-                   return_lse, workspace, status):
-    tokens, heads, d = q.shape
-    dev = q.device
-    if out is None:
-        out = q.new_empty((tokens, heads, d))
-        ldo = heads * d
-    else:
-        ldo = _rows_of(out, "out", 3, {q.dtype: 0})
-        if out.shape != q.shape:
-            raise ValueError(f"out must have shape {tuple(q.shape)}")
-    lse = q.new_empty((tokens, heads), dtype=torch.float32) if return_lse else None
-    ws = _work(kv8_attention_workspace_bytes(tokens, heads, c[5], d, batch, max_new, max_len,
-                                             window), dev, workspace)
-    _check(load_library().piq_kv8_attention(
-        q.data_ptr(), _HALF[q.dtype], tokens, ldq, heads, cu.data_ptr(), lens.data_ptr(), batch,
-        *table, *c, d ** -0.5 if scale is None else float(scale), window, max_new, max_len,
-        out.data_ptr(), ldo, None if lse is None else lse.data_ptr(), _status_ptr(status, dev),
-        ws.data_ptr(), ws.numel(), s), "piq_kv8_attention")
-    return (out, lse) if return_lse else out
+    return (_serve or _serving()).kv8_attention(
+        *cache, q, cu, lens, block_table, max_new, max_len, scale, window, return_lse, out,
+        _handle(stream), workspace, status)

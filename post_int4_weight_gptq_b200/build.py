@@ -1,4 +1,6 @@
-"""Build the in-tree shared library ``lib/libpiq.so`` with nvcc for sm_100a.
+"""Build the in-tree shared libraries with nvcc and g++: ``lib/libpiq.so`` (the
+kernels and the C ABI, sm_100a) and ``lib/piq_serve.so`` (the Python entry of the
+8-bit serving calls, ``csrc/serve_binding.cpp``, against torch's headers).
 
 Usage: ``python -m post_int4_weight_gptq_b200.build [--force] [--verbose]``.
 Sources are ``csrc/*.cu``; the C ABI is ``include/piq.h`` at the repository
@@ -13,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "lib")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(LIBDIR, "libpiq.so")
+SERVE = os.path.join(LIBDIR, "piq_serve.so")
+SERVE_SRC = os.path.join(CSRC, "serve_binding.cpp")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -50,8 +55,33 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def build_serve(force: bool = False) -> str:
+    """The serving binding; needs libpiq.so to link to."""
+    if not force and os.path.exists(SERVE) and all(
+            os.path.getmtime(p) <= os.path.getmtime(SERVE)
+            for p in (SERVE_SRC, os.path.join(INCLUDE, "piq.h"))):
+        return SERVE
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = SERVE + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", SERVE_SRC, "-o", tmp,
+           "-I" + os.path.join(base, "include"),
+           "-I" + os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-I" + os.path.join(cuda, "include"), "-I" + sysconfig.get_paths()["include"],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu",
+           "-lc10_cuda", "-lc10", "-L" + LIBDIR, "-lpiq", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {os.path.basename(SERVE_SRC)}:\n{r.stderr}")
+    os.replace(tmp, SERVE)
+    return SERVE
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     if not force and up_to_date():
+        build_serve()
         return LIB
     os.makedirs(LIBDIR, exist_ok=True)
     os.makedirs(OBJDIR, exist_ok=True)
@@ -77,6 +107,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    build_serve(force)
     return LIB
 
 
