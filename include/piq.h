@@ -412,7 +412,8 @@ int piq_int8_quantize_rows(const void* X, int dtype, int64_t rows, int64_t cols,
  *   Y        device [tokens, out] of X's dtype, row stride ldy >= out.
  * tokens >= 0; in % 8 == 0, 8 <= in <= 131064 (the int32 sums stay exact for
  * every code, -128 among them); 1 <= out <= 2^24.
- * Workspace: piq_int8_linear_workspace_bytes. */
+ * Workspace: piq_int8_linear_workspace_bytes (0 for a few tokens: then it may be
+ * NULL). */
 int piq_int8_linear_workspace_bytes(int64_t tokens, int64_t out, int64_t in, size_t* bytes);
 int piq_int8_linear(const void* X, int dtype, int64_t tokens, int64_t in, int64_t ldx,
                     const int8_t* W, int64_t out, int64_t ldw, const float* w_scale,

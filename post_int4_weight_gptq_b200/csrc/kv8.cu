@@ -54,11 +54,16 @@ __device__ __forceinline__ int find_item(const int32_t* cu, int batch, int block
   return lo - 1;
 }
 
-// One block of tokens of one head, keys (blockIdx.z == 0) or values (1): NR
-// runs of eight values a thread, read once, the block's scale found by a
-// reduction over the CTA, codes written from the registers.
+// One block of tokens of one head, keys (blockIdx.z == 0) or values (1).
+// NR > 0: NR runs of eight values a thread, the whole block read once, its scale
+// found by a reduction over the CTA, codes written from the registers.
+// NR == 0, for calls of a few tokens a sequence: only the new tokens' runs are
+// visited, twice (the second time from the cache), in few registers, so that the
+// CTAs of a decoding step fit the machine at once.
+// The tokens are asked for before the page they go to is looked up.
 template <typename T, int D, int NR>
 __global__ void __launch_bounds__(256) kv8_append_kernel(Kv8Write p) {
+  constexpr int RPT = D / 8;  // runs a token
   __shared__ uint32_t red[8];
   pdl_launch_dependents();
   pdl_wait();
@@ -74,45 +79,54 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(Kv8Write p) {
     if (threadIdx.x == 0) note_status(p.status, PIQ_ERR_INVALID_ARG, b);
     return;
   }
-  const int64_t first_block = before / p.block;
-  const int64_t blk = first_block + (blockIdx.x - item_start(p.cu, b, p.block));
-  const int64_t base = blk * p.block;              // position of the block's first token
+  const int shift = __ffs(p.block) - 1;
+  const int64_t blk = (before >> shift) + (blockIdx.x - item_start(p.cu, b, p.block));
+  const int64_t base = blk << shift;               // position of the block's first token
   const int64_t end = before + (row1 - row0);      // the sequence's tokens after this call
   if (base >= end) return;
-  const int64_t page = __ldg(p.table + b * p.ldt + blk);
-  if (page < 0 || page >= p.pages) {
-    if (threadIdx.x == 0) note_status(p.status, PIQ_ERR_INVALID_ARG, b);
-    return;
-  }
-  const int o0 = static_cast<int>(max(before, base) - base);       // first new token
+  const int o0 = static_cast<int>(max(before, base) - base);         // first new token
   const int o1 = static_cast<int>(min(end, base + p.block) - base);  // behind the last one
   const bool vals = blockIdx.z != 0;
   const int64_t ld = vals ? p.ldv : p.ldk;
   const T* src = static_cast<const T*>(vals ? p.v : p.k) +
                  (row0 + (base - before)) * ld + head * D;  // the block's token 0, if it is new
-  int8_t* dst = (vals ? p.vc : p.kc) + (page * p.heads + head) * p.block * static_cast<int64_t>(D);
-  float* sp = (vals ? p.vs : p.ks) + page * p.heads + head;
 
-  Eight<T> v[NR];
+  Eight<T> v[NR > 0 ? NR : 1];
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
     const int run = threadIdx.x + i * blockDim.x;
-    const int o = run / (D / 8);
+    const int o = run / RPT;
     if (o >= o0 && o < o1)
-      v[i].load(src + o * ld + (run % (D / 8)) * 8);
+      v[i].load(src + o * ld + (run % RPT) * 8);
     else
       v[i].zero();
   }
+  const int64_t page = __ldg(p.table + b * p.ldt + blk);
+  if (page < 0 || page >= p.pages) {
+    if (threadIdx.x == 0) note_status(p.status, PIQ_ERR_INVALID_ARG, b);
+    return;
+  }
+  int8_t* dst = (vals ? p.vc : p.kc) + (page * p.heads + head) * p.block * static_cast<int64_t>(D);
+  float* sp = (vals ? p.vs : p.ks) + page * p.heads + head;
+  const float old = o0 > 0 ? *sp : 0.0f;  // read before thread 0 writes it, below the barrier
+  if (NR > 0) {
 #pragma unroll
-  for (int i = 0; i < NR; ++i) {
-    float f[8];
-    v[i].floats(f);
-    m = amax_bits8(f, m);
+    for (int i = 0; i < NR; ++i) {
+      float f[8];
+      v[i].floats(f);
+      m = amax_bits8(f, m);
+    }
+  } else {
+    for (int run = o0 * RPT + threadIdx.x; run < o1 * RPT; run += blockDim.x) {
+      float f[8];
+      v[0].load(src + (run / RPT) * ld + (run % RPT) * 8);
+      v[0].floats(f);
+      m = amax_bits8(f, m);
+    }
   }
   m = __reduce_max_sync(0xffffffffu, m);
   if (lane == 0) red[threadIdx.x >> 5] = m;
-  const float old = o0 > 0 ? *sp : 0.0f;  // read before thread 0 writes it, below the barrier
   __syncthreads();
   m = red[lane % (blockDim.x / 32)];
   m = __reduce_max_sync(0xffffffffu, m);
@@ -120,27 +134,35 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(Kv8Write p) {
   if (!(scale >= old) && scale == scale) scale = old;  // the larger one; NaN of either stays
   const float inv = inverse_of(scale);
   if (threadIdx.x == 0) *sp = scale;
-  // codes already there: unchanged while the scale is
-  const bool requant = o0 > 0 && !(scale == old);
-  const float ratio = scale > 0.0f ? __fdiv_rn(old, scale) : 0.0f;
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
     const int run = threadIdx.x + i * blockDim.x;
-    const int o = run / (D / 8);
-    int8_t* at = dst + run * 8;
+    const int o = run / RPT;
     if (o >= o0 && o < o1) {
       float f[8];
       v[i].floats(f);
-      *reinterpret_cast<uint2*>(at) = codes8(f, inv);
-    } else if (requant && o < o0) {
-      const uint2 c = *reinterpret_cast<const uint2*>(at);
+      *reinterpret_cast<uint2*>(dst + run * 8) = codes8(f, inv);
+    }
+  }
+  if (NR == 0)
+    for (int run = o0 * RPT + threadIdx.x; run < o1 * RPT; run += blockDim.x) {
+      float f[8];
+      v[0].load(src + (run / RPT) * ld + (run % RPT) * 8);
+      v[0].floats(f);
+      *reinterpret_cast<uint2*>(dst + run * 8) = codes8(f, inv);
+    }
+  // codes already there: unchanged while the scale is
+  if (o0 > 0 && !(scale == old)) {
+    const float ratio = scale > 0.0f ? __fdiv_rn(old, scale) : 0.0f;
+    for (int run = threadIdx.x; run < o0 * RPT; run += blockDim.x) {
+      const uint2 c = *reinterpret_cast<const uint2*>(dst + run * 8);
       float f[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         f[j] = static_cast<float>(static_cast<int8_t>(c.x >> (8 * j)));
         f[4 + j] = static_cast<float>(static_cast<int8_t>(c.y >> (8 * j)));
       }
-      *reinterpret_cast<uint2*>(at) = codes8(f, ratio);
+      *reinterpret_cast<uint2*>(dst + run * 8) = codes8(f, ratio);
     }
   }
 }
@@ -171,14 +193,15 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(Kv8Read p) {
   if (b < 0) return;
   const int64_t pos = __ldg(p.start + b) + (row - __ldg(p.cu + b));
   int64_t page = -1;
-  if (pos >= 0 && pos < p.width * p.block) page = __ldg(p.table + b * p.ldt + pos / p.block);
+  const int shift = __ffs(p.block) - 1;
+  if (pos >= 0 && pos < p.width * p.block) page = __ldg(p.table + b * p.ldt + (pos >> shift));
   const bool bad = page < 0 || page >= p.pages;
   if (bad && lane == 0) note_status(p.status, PIQ_ERR_INVALID_ARG, b);
   const bool vals = blockIdx.y != 0;
   const int8_t* codes = vals ? p.vc : p.kc;
   const float* scales = vals ? p.vs : p.ks;
   T* out = static_cast<T*>(vals ? p.v : p.k) + row * (vals ? p.ldv : p.ldk);
-  const int off = static_cast<int>(pos % p.block);
+  const int off = static_cast<int>(pos) & (p.block - 1);
   for (int run = lane; run < p.heads * (D / 8); run += 32) {
     const int head = run / (D / 8), d = (run % (D / 8)) * 8;
     uint2 c = make_uint2(0u, 0u);
@@ -201,12 +224,17 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(Kv8Read p) {
   }
 }
 
+// New tokens a sequence, on average, up to which most of a block is not new.
+constexpr int64_t kFewNew = 4;
+
 template <typename T, int D>
 int launch_append(const Kv8Write& p, cudaStream_t stream) {
   const int runs = p.block * (D / 8);  // 128 .. 2048
-  const int threads = runs > 1024 ? 256 : 128;
+  const bool few = p.tokens <= kFewNew * p.batch;
+  const int threads = !few && runs > 1024 ? 256 : 128;
   void (*kern)(Kv8Write) = nullptr;
-  switch (runs / threads) {
+  switch (few ? 0 : runs / threads) {
+    case 0: kern = kv8_append_kernel<T, D, 0>; break;
     case 1: kern = kv8_append_kernel<T, D, 1>; break;
     case 2: kern = kv8_append_kernel<T, D, 2>; break;
     case 4: kern = kv8_append_kernel<T, D, 4>; break;

@@ -133,6 +133,7 @@ int32_t* status_of(PyObject* o, const at::Device& dev) {
 
 // The caller's workspace if it is large enough, else a new one.
 at::Tensor workspace_of(PyObject* o, size_t bytes, const at::Device& dev) {
+  if (bytes == 0) return at::Tensor();
   if (o != Py_None) {
     const at::Tensor& t = cuda_tensor(o, "workspace");
     need_type(t, at::kByte, "workspace");
@@ -234,7 +235,8 @@ PyObject* linear(PyObject* const* a) {
         "piq_int8_linear_workspace_bytes");
   const at::Tensor ws = workspace_of(a[6], bytes, dev);
   check(piq_int8_linear(x.data_ptr(), dtype, tokens, in, ldx, w.data_ptr<int8_t>(), out, ldw, sw,
-                        bias, y.data_ptr(), ldy, status, ws.data_ptr(), ws.numel(), on.stream()),
+                        bias, y.data_ptr(), ldy, status, ws.defined() ? ws.data_ptr() : nullptr,
+                        bytes, on.stream()),
         "piq_int8_linear");
   return THPVariable_Wrap(y);
 }
@@ -331,8 +333,8 @@ PyObject* attention(PyObject* const* a) {
                           static_cast<int>(c.heads), static_cast<int>(c.dim),
                           static_cast<int>(c.block), static_cast<float>(scale),
                           static_cast<int>(window), max_new, max_len, out.data_ptr(), ldo,
-                          truth ? lse.data_ptr<float>() : nullptr, status, ws.data_ptr(),
-                          ws.numel(), on.stream()),
+                          truth ? lse.data_ptr<float>() : nullptr, status, ws.data_ptr(), bytes,
+                          on.stream()),
         "piq_kv8_attention");
   if (!truth) return THPVariable_Wrap(out);
   return Py_BuildValue("NN", THPVariable_Wrap(out), THPVariable_Wrap(lse));

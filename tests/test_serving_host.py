@@ -37,7 +37,7 @@ def test_quantize_no_rows_is_nothing(lib):
     assert quantize(lib, rows=0, X=None, codes=None, scales=None) == piq.PIQ_OK
 
 
-def linear(lib, X=FAKE, dtype=0, tokens=4, inp=64, ldx=64, W=FAKE, out=32, ldw=64, ws=FAKE,
+def linear(lib, X=FAKE, dtype=0, tokens=40, inp=64, ldx=64, W=FAKE, out=32, ldw=64, ws=FAKE,
            bias=None, Y=FAKE, ldy=32, status=None, work=FAKE, nbytes=1 << 20):
     return lib.piq_int8_linear(X, dtype, tokens, inp, ldx, W, out, ldw, ws, bias, Y, ldy, status,
                                work, nbytes, None)
@@ -57,8 +57,12 @@ def test_linear_refuses(lib, kw):
 def test_linear_workspace(lib):
     assert linear(lib, nbytes=0) == piq.PIQ_ERR_WORKSPACE_TOO_SMALL
     assert linear(lib, tokens=0, X=None, Y=None, work=None) == piq.PIQ_OK
-    a, b = piq.int8_linear_workspace_bytes(4, 32, 64), piq.int8_linear_workspace_bytes(400, 32, 64)
+    a, b = piq.int8_linear_workspace_bytes(40, 32, 64), piq.int8_linear_workspace_bytes(400, 32, 64)
     assert 0 < a <= b
+    # a few tokens run as one kernel without a workspace; long rows or more tokens do not
+    assert piq.int8_linear_workspace_bytes(4, 32, 4096) == 0
+    assert piq.int8_linear_workspace_bytes(4, 32, 4104) > 0
+    assert piq.int8_linear_workspace_bytes(5, 32, 64) > 0
     out = ctypes.c_size_t()
     assert lib.piq_int8_linear_workspace_bytes(4, 32, 60, ctypes.byref(out)) < 0
     assert lib.piq_int8_linear_workspace_bytes(4, 32, 64, None) < 0
