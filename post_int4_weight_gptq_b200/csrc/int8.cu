@@ -40,7 +40,6 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
   const T* x = X + (live ? row : 0) * ldx;
   const int64_t runs = live ? cols / 8 : 0;
   Eight<T> v[kRuns];
-  uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < kRuns; ++i) {
     const int64_t r = tr + static_cast<int64_t>(i) * TPR;
@@ -49,19 +48,15 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
     else
       v[i].zero();
   }
+  Largest<T> top;
 #pragma unroll
-  for (int i = 0; i < kRuns; ++i) {
-    float f[8];
-    v[i].floats(f);
-    m = amax_bits8(f, m);
-  }
+  for (int i = 0; i < kRuns; ++i) top.add(v[i]);
   for (int64_t r = tr + static_cast<int64_t>(kRuns) * TPR; r < runs; r += TPR) {
     Eight<T> e;
-    float f[8];
     e.load(x + 8 * r);
-    e.floats(f);
-    m = amax_bits8(f, m);
+    top.add(e);
   }
+  uint32_t m = top.bits();
   m = __reduce_max_sync(0xffffffffu, m);
   if (TPR > 32) {
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
@@ -175,20 +170,18 @@ __global__ void __launch_bounds__(32 * kFewWarps)
   const float sc = c < out ? __ldg(sw + c) : 0.0f;
   const float bc = bias != nullptr && c < out ? __ldg(bias + c) : 0.0f;
 
-  uint32_t m[TOK] = {};
+  Largest<T> top[TOK];
   for (int k = 8 * threadIdx.x; k < in; k += 8 * 32 * kFewWarps)
 #pragma unroll
     for (int t = 0; t < TOK; ++t) {
       Eight<T> e;
-      float f[8];
       e.load(X + min(t, tokens - 1) * ldx + k);
-      e.floats(f);
-      m[t] = amax_bits8(f, m[t]);
+      top[t].add(e);
     }
 #pragma unroll
   for (int t = 0; t < TOK; ++t) {
-    m[t] = __reduce_max_sync(0xffffffffu, m[t]);
-    if (lane == 0) red[t][warp] = m[t];
+    const uint32_t m = __reduce_max_sync(0xffffffffu, top[t].bits());
+    if (lane == 0) red[t][warp] = m;
   }
   __syncthreads();
   float scale[TOK], inv[TOK];
@@ -239,7 +232,7 @@ __global__ void __launch_bounds__(32 * kFewWarps)
 
 // Tokens that the kernel above takes: its CTAs all quantize them, which stops
 // paying when that reads as much as a CTA's weights.
-constexpr int64_t kFewTokens = 4, kFewValues = 16384;
+constexpr int64_t kFewTokens = 1, kFewValues = 16384;
 bool few_tokens(int64_t tokens, int64_t in) {
   return tokens <= kFewTokens && tokens * in <= kFewValues;
 }

@@ -40,7 +40,10 @@ constexpr int BM = 128;               // channels a CTA
 constexpr int BK = 128;               // bytes of k a stage: one swizzled row
 constexpr int A_TILE = BM * BK;       // 16 KB
 constexpr int kRing = 192 * 1024;     // bytes of all stages
-constexpr int kSmem = kRing + 1024 + 1024;  // alignment, barriers
+constexpr int kSmallRing = 96 * 1024; // of the split kernel on up to 64 tokens: two CTAs share
+                                      // a multiprocessor, one starting while the other ends
+constexpr int kSmemExtra = 1024 + 1024;  // alignment, barriers
+constexpr int split_ring(int nt) { return nt <= 64 ? kSmallRing : kRing; }
 
 struct GemmArgs {
   int tokens, in, out;
@@ -49,6 +52,7 @@ struct GemmArgs {
   const float *sx, *sw, *bias;
   void* Y;
   int64_t ldy;
+  bool wide;  // Y and its rows are 16-byte aligned
   int32_t* status;
 };
 
@@ -65,9 +69,11 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
   return a;
 }
-__device__ __forceinline__ int ld_cluster(uint32_t addr) {
-  int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr));
+__device__ __forceinline__ int4 ld_cluster(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
   return v;
 }
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
@@ -97,29 +103,62 @@ __device__ __forceinline__ void umma_s8(uint32_t tmem_d, uint64_t adesc, uint64_
         : "memory");
 }
 
-template <typename T>
-__device__ __forceinline__ void put(const GemmArgs& p, int t, int c, int acc, float sx, float sw,
-                                    float bias) {
-  if (t < p.tokens && c < p.out)
-    static_cast<T*>(p.Y)[t * p.ldy + c] =
-        from_float<T>(fmaf(static_cast<float>(acc) * sx, sw, bias));
+__device__ __forceinline__ float scaled(int acc, float sx, float sw, float bias) {
+  return fmaf(static_cast<float>(acc) * sx, sw, bias);
+}
+
+// N tokens (t0 ..) of a warp's 32 channels (c0 .., one a lane, accumulators in f) to
+// Y through the warp's staging rows: a lane holds a channel of every token, a store
+// wants neighbouring channels of one.  Stores of one channel a lane took the tile of
+// 256 tokens 6 us; this takes an eighth of their instructions.
+template <typename T, int N>
+__device__ __forceinline__ void store_tokens(const GemmArgs& p, T* stage, const float (&f)[N],
+                                             const float4* sx4, int t0, int c0, float sw,
+                                             float bias, int lane) {
+  constexpr int PER = 16 / sizeof(T), PIECES = 32 / PER;  // channels a piece, pieces a token
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const float4 s = sx4[i];
+    stage[(4 * i) * 32 + lane] = from_float<T>(scaled(__float_as_int(f[4 * i]), s.x, sw, bias));
+    stage[(4 * i + 1) * 32 + lane] = from_float<T>(scaled(__float_as_int(f[4 * i + 1]), s.y, sw, bias));
+    stage[(4 * i + 2) * 32 + lane] = from_float<T>(scaled(__float_as_int(f[4 * i + 2]), s.z, sw, bias));
+    stage[(4 * i + 3) * 32 + lane] = from_float<T>(scaled(__float_as_int(f[4 * i + 3]), s.w, sw, bias));
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < N * PIECES / 32; ++i) {
+    const int piece = i * 32 + lane, t = t0 + piece / PIECES, c = c0 + piece % PIECES * PER;
+    const uint4 v = reinterpret_cast<const uint4*>(stage)[piece];
+    T* y = static_cast<T*>(p.Y) + t * p.ldy + c;
+    if (t < p.tokens) {
+      if (p.wide && c + PER <= p.out) {
+        *reinterpret_cast<uint4*>(y) = v;
+      } else {
+        const T* e = stage + piece * PER;
+        for (int j = 0; j < PER && c + j < p.out; ++j) y[j] = e[j];
+      }
+    }
+  }
+  __syncwarp();
 }
 
 // ------------------------------------------------------------------- split
 template <typename T, int NT>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(192, NT <= 64 ? 2 : 1)
     int8_split_kernel(const __grid_constant__ CUtensorMap tmW,
                       const __grid_constant__ CUtensorMap tmX, GemmArgs p) {
+  constexpr int RING = split_ring(NT);
   constexpr int STAGE = A_TILE + NT * BK;
-  constexpr int STAGES = kRing / STAGE;
+  constexpr int STAGES = RING / STAGE;
   constexpr uint32_t COLS = NT < 32 ? 32 : NT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRing);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + RING);
   uint64_t* empty = full + STAGES;
   uint64_t* done = empty + STAGES;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  __shared__ __align__(16) float s_sx[NT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slices = p.slices, slice = blockIdx.x % slices;  // a cluster is one tile's slices
   const int c0 = blockIdx.x / slices * BM, t0 = blockIdx.y * NT;
@@ -192,22 +231,29 @@ __global__ void __launch_bounds__(192, 1)
     const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const float sw = c < p.out ? __ldg(p.sw + c) : 0.0f;
     const float bias = p.bias != nullptr && c < p.out ? __ldg(p.bias + c) : 0.0f;
-    const bool ok = wait_bar(done, 0, p.status, 63);
+    // the tokens' scales, for all four warps
+    for (int i = threadIdx.x - 64; i < NT; i += 128)
+      s_sx[i] = __ldg(p.sx + min(t0 + i, p.tokens - 1));
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    const bool ok = wait_warp(done, 0, p.status, 63);
     tc_fence_after();
-    int* part = reinterpret_cast<int*>(smem);  // [NT][BM], the ring is empty now
+    // the ring is empty now: staging of the stores, or this slice's sums [NT][BM]
+    constexpr int CH = NT < 32 ? NT : 32;
+    T* const stage = reinterpret_cast<T*>(smem) + q * (CH * 32);
+    int* const part = reinterpret_cast<int*>(smem);
     if (ok) {
-      for (int n = 0; n < NT && t0 + n < p.tokens; n += 16) {
-        float f[16];
-        tmem_ld_32x32b_x16(taddr + n, f);
+      for (int n = 0; n < NT && t0 + n < p.tokens; n += CH) {
+        float f[CH];
+        if constexpr (CH == 32)
+          tmem_ld_32x32b_x32(taddr + n, f);
+        else
+          tmem_ld_32x32b_x16(taddr + n, f);
         if (slices == 1) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int t = t0 + n + i;
-            put<T>(p, t, c, __float_as_int(f[i]), __ldg(p.sx + min(t, p.tokens - 1)), sw, bias);
-          }
+          store_tokens<T, CH>(p, stage, f, reinterpret_cast<const float4*>(s_sx + n), t0 + n,
+                              c0 + q * 32, sw, bias, lane);
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) part[(n + i) * BM + ch] = __float_as_int(f[i]);
+          for (int i = 0; i < CH; ++i) part[(n + i) * BM + ch] = __float_as_int(f[i]);
         }
       }
     }
@@ -216,22 +262,48 @@ __global__ void __launch_bounds__(192, 1)
   __syncthreads();
   if (slices > 1) {
     cluster_sync();
-    // this CTA's share of the tokens, every slice's part of them
+    // this CTA's share of the tokens: a warp a token, four channels a lane, every
+    // slice's sums read at once
     if (warp >= 2) {
-      const int ch = (warp - 2) * 32 + lane, c = c0 + ch;
-      const float sw = c < p.out ? __ldg(p.sw + c) : 0.0f;
-      const float bias = p.bias != nullptr && c < p.out ? __ldg(p.bias + c) : 0.0f;
+      const int c = c0 + 4 * lane;
+      float sw[4], bias[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sw[j] = c + j < p.out ? __ldg(p.sw + c + j) : 0.0f;
+        bias[j] = p.bias != nullptr && c + j < p.out ? __ldg(p.bias + c + j) : 0.0f;
+      }
       const int live = min(NT, p.tokens - t0);
-      const uint32_t base = smem_u32(smem) + 4 * ch;
-      for (int n = slice; n < live; n += slices) {
-        int v[8];
+      const uint32_t base = smem_u32(smem) + 16 * lane;
+#pragma unroll 2
+      for (int n = slice + slices * (warp - 2); n < live; n += 4 * slices) {
+        int4 v[8];
 #pragma unroll
         for (int s = 0; s < 8; ++s)
-          v[s] = s < slices ? ld_cluster(map_rank(base + 4 * BM * n, s)) : 0;
-        int acc = 0;
+          v[s] = s < slices ? ld_cluster(map_rank(base + 4 * BM * n, s)) : make_int4(0, 0, 0, 0);
+        int4 a = v[0];
 #pragma unroll
-        for (int s = 0; s < 8; ++s) acc += v[s];
-        put<T>(p, t0 + n, c, acc, __ldg(p.sx + t0 + n), sw, bias);
+        for (int s = 1; s < 8; ++s) {
+          a.x += v[s].x;
+          a.y += v[s].y;
+          a.z += v[s].z;
+          a.w += v[s].w;
+        }
+        const float sx = s_sx[n];
+        T y[4] = {from_float<T>(scaled(a.x, sx, sw[0], bias[0])),
+                  from_float<T>(scaled(a.y, sx, sw[1], bias[1])),
+                  from_float<T>(scaled(a.z, sx, sw[2], bias[2])),
+                  from_float<T>(scaled(a.w, sx, sw[3], bias[3]))};
+        T* to = static_cast<T*>(p.Y) + (t0 + n) * p.ldy + c;
+        if (p.wide && c + 4 <= p.out) {
+          if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<float4*>(to) = make_float4(y[0], y[1], y[2], y[3]);
+          else
+            *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(y);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (c + j < p.out) to[j] = y[j];
+        }
       }
     }
     cluster_sync();  // nobody leaves while its part is read
@@ -375,6 +447,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpi, 1)
   } else {
     const int q = warp & 3, h = (warp - 2) >> 2;
     const uint32_t free_bar = map_rank(smem_u32(acc_empty), 0);
+    T* const stage = reinterpret_cast<T*>(smem + kRing + 1024) + (warp - 2) * (32 * 32);
     int lt = 0;
     for (int t = pair; t < tiles; t += pairs, ++lt) {
       int m, n;
@@ -383,32 +456,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpi, 1)
       const int c = (2 * m + static_cast<int>(rank)) * BM + q * 32 + lane;
       const float sw = c < p.out ? __ldg(p.sw + c) : 0.0f;
       const float bias = p.bias != nullptr && c < p.out ? __ldg(p.bias + c) : 0.0f;
-      if (!wait_bar(&acc_full[buf], (lt >> 1) & 1, p.status, 67)) break;
+      if (!wait_warp(&acc_full[buf], (lt >> 1) & 1, p.status, 67)) break;
       tc_fence_after();
       const int t0 = n * NT + h * (NT / 2);
       const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * NT + h * (NT / 2);
-      for (int i0 = 0; i0 < NT / 2; i0 += 32) {
+      for (int i0 = 0; i0 < NT / 2 && t0 + i0 < p.tokens; i0 += 32) {
         float f[32];
         tmem_ld_32x32b_x32(taddr + i0, f);
+        float4 sx[8];
         if (t0 + i0 + 32 <= p.tokens) {
-          const float4* sx4 = reinterpret_cast<const float4*>(p.sx + t0 + i0);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 s = __ldg(sx4 + i);
-            const int tt = t0 + i0 + 4 * i;
-            put<T>(p, tt, c, __float_as_int(f[4 * i]), s.x, sw, bias);
-            put<T>(p, tt + 1, c, __float_as_int(f[4 * i + 1]), s.y, sw, bias);
-            put<T>(p, tt + 2, c, __float_as_int(f[4 * i + 2]), s.z, sw, bias);
-            put<T>(p, tt + 3, c, __float_as_int(f[4 * i + 3]), s.w, sw, bias);
-          }
+          for (int i = 0; i < 8; ++i) sx[i] = __ldg(reinterpret_cast<const float4*>(p.sx + t0 + i0) + i);
         } else {
+          const int last = p.tokens - 1, at = t0 + i0;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int tt = t0 + i0 + i;
-            if (tt < p.tokens)
-              put<T>(p, tt, c, __float_as_int(f[i]), __ldg(p.sx + tt), sw, bias);
-          }
+          for (int i = 0; i < 8; ++i)
+            sx[i] = make_float4(__ldg(p.sx + min(at + 4 * i, last)), __ldg(p.sx + min(at + 4 * i + 1, last)),
+                                __ldg(p.sx + min(at + 4 * i + 2, last)), __ldg(p.sx + min(at + 4 * i + 3, last)));
         }
+        store_tokens<T, 32>(p, stage, f, sx, t0 + i0, c - lane, sw, bias, lane);
       }
       tc_fence_before();
       __syncwarp();
@@ -443,26 +509,27 @@ bool code_map(CUtensorMap* map, const int8_t* q, int64_t rows, int64_t cols, int
 typedef void (*GemmKernel)(CUtensorMap, CUtensorMap, GemmArgs);
 
 // The shared-memory limit of each kernel, raised once on each device.
-int raise_smem(GemmKernel kern, int slot) {
+int raise_smem(GemmKernel kern, int slot, int smem) {
   static std::atomic<bool> set[64][32];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return PIQ_ERR_CUDA;
   if (dev < 64 && set[dev][slot].load(std::memory_order_acquire)) return PIQ_OK;
   const int rc = cuda_rc(
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   if (rc == PIQ_OK && dev < 64) set[dev][slot].store(true, std::memory_order_release);
   return rc;
 }
 
-int launch_gemm(GemmKernel kern, int slot, dim3 grid, int threads, int cluster,
+int launch_gemm(GemmKernel kern, int slot, dim3 grid, int threads, int ring, int cluster,
                 cudaStream_t stream, const CUtensorMap& mw, const CUtensorMap& mx,
                 const GemmArgs& p) {
-  const int rc = raise_smem(kern, slot);
+  const int smem = ring + kSmemExtra;
+  const int rc = raise_smem(kern, slot, smem);
   if (rc != PIQ_OK) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -497,13 +564,14 @@ int gemm_t(const int8_t* qx, int64_t ldq, const int8_t* W, int64_t ldw, GemmArgs
     if (tiles > INT32_MAX) return PIQ_ERR_INVALID_ARG;
     const int pairs = static_cast<int>(std::min<int64_t>(tiles, sms / 2));
     const int i = a.nt == 256;
-    return launch_gemm(pair[i], slot0 + i, dim3(2 * pairs), 64 + 32 * kEpi, 0, stream, mw, mx, p);
+    return launch_gemm(pair[i], slot0 + i, dim3(2 * pairs), 64 + 32 * kEpi,
+                       kRing + kEpi * 32 * 32 * static_cast<int>(sizeof(T)), 0, stream, mw, mx, p);
   }
   p.m_tiles = static_cast<int>(ceil_div(p.out, BM));
   p.slices = a.slices;
   int i = 0;
   while (16 << i < a.nt) ++i;
-  return launch_gemm(split[i], slot0 + 2 + i, dim3(a.slices * p.m_tiles, p.n_tiles), 192, a.slices,
+  return launch_gemm(split[i], slot0 + 2 + i, dim3(a.slices * p.m_tiles, p.n_tiles), 192, split_ring(a.nt), a.slices,
                      stream, mw, mx, p);
 }
 
@@ -522,27 +590,50 @@ EncodeTiledFn tensor_map_encoder() {
   return fn;
 }
 
-// Tiles of one product.  Many tokens: pairs, on 256-token tiles when those give
-// every pair of multiprocessors work, else on 128-token tiles while they do.
-// Fewer: single CTAs, the widest token tile that still gives most multiprocessors a
-// tile, and k cut into up to eight slices (each at least four 128-byte steps)
-// when the tiles alone do not.
+// Tiles of one product.  The forms differ in the tiles that run at once and in the
+// time of one tile (relative, measured at in = 4096: 256 x 256 on a pair 4.0, 256 x
+// 128 3.0, 128 x 256 on one CTA 4.2, 128 x 128 3.1, 128 x 64 with two CTAs a
+// multiprocessor 2.9); the one with the least waves times time is taken.  1024 x 4096
+// -> 4096 took 20.6 us on pairs of 256, 26.0 on pairs of 128, 29.2 on 64; 512 tokens
+// 19.4, 17.0 and 15.6.  Up to 64 tokens fit one tile, as narrow as they are.  Where
+// the tiles leave multiprocessors idle, k is cut into up to eight slices of at least
+// eight 128-byte steps (37 x 11008 -> 4096: 29 us whole, 14 us in eight; 64 x 4096 ->
+// 11008, 86 tiles, gains nothing from two and loses with four).
 Int8Plan plan_int8(int64_t tokens, int64_t out, int64_t in, int sms) {
   Int8Plan a;
-  const int64_t mp = ceil_div(out, 2 * BM), m1 = ceil_div(out, BM);
-  a.pair = true;
-  a.slices = 1;
-  a.nt = 256;
-  if (tokens > 128 && mp * ceil_div(tokens, 256) >= sms / 2) return a;
-  a.nt = 128;
-  if (tokens > 128 && mp * ceil_div(tokens, 128) >= sms / 2 * 3 / 4) return a;
   a.pair = false;
-  a.nt = 256;
-  while (a.nt > 16 && (ceil_div(tokens, a.nt / 2) == 1 ||
-                       (a.nt > 64 && m1 * ceil_div(tokens, a.nt) < sms * 3 / 4)))
-    a.nt /= 2;
-  const int64_t tiles = m1 * ceil_div(tokens, a.nt), kb = ceil_div(in, BK);
-  while (a.slices < 8 && tiles * a.slices * 2 <= sms && kb >= 8 * a.slices) a.slices *= 2;
+  a.slices = 1;
+  a.nt = 64;
+  const int64_t m1 = ceil_div(out, BM), m2 = ceil_div(out, 2 * BM);
+  if (tokens > 64) {
+    struct Form {
+      bool pair;
+      int nt, at_once, time;
+    };
+    const Form forms[] = {{false, 64, 2 * sms, 29},
+                          {false, 128, sms, 31},
+                          {true, 128, sms / 2, 30},
+                          {true, 256, sms / 2, 40},
+                          {false, 256, sms, 42}};
+    int64_t best = INT64_MAX;
+    for (const Form& f : forms) {
+      const int64_t tiles = (f.pair ? m2 : m1) * ceil_div(tokens, f.nt);
+      const int64_t t = ceil_div(tiles, f.at_once) * f.time;
+      // (the grid's second dimension holds the split kernel's token tiles)
+      if (t < best && (f.pair || ceil_div(tokens, f.nt) <= 65535)) {
+        best = t;
+        a.pair = f.pair;
+        a.nt = f.nt;
+      }
+    }
+  } else {
+    while (a.nt > 16 && tokens <= a.nt / 2) a.nt /= 2;
+  }
+  if (!a.pair) {
+    const int64_t tiles = m1 * ceil_div(tokens, a.nt), kb = ceil_div(in, BK);
+    const int64_t room = a.nt <= 64 ? 2 * sms : sms;
+    while (a.slices < 8 && tiles * a.slices * 2 <= room && kb >= 16 * a.slices) a.slices *= 2;
+  }
   return a;
 }
 
@@ -561,6 +652,8 @@ int launch_int8_gemm(const int8_t* qx, int64_t ldq, const float* sx, int64_t tok
   p.bias = bias;
   p.Y = Y;
   p.ldy = ldy;
+  const int size = dtype == PIQ_FP32 ? 4 : 2;
+  p.wide = ptr_aligned(Y, 16) && ldy * size % 16 == 0;
   p.status = status;
   switch (dtype) {
     case PIQ_BF16: return gemm_t<__nv_bfloat16>(qx, ldq, W, ldw, p, stream, info.sm_count);

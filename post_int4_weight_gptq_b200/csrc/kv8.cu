@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(Kv8Write p) {
                  (row0 + (base - before)) * ld + head * D;  // the block's token 0, if it is new
 
   Eight<T> v[NR > 0 ? NR : 1];
-  uint32_t m = 0;
+  Largest<T> top;
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
     const int run = threadIdx.x + i * blockDim.x;
@@ -112,20 +112,14 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(Kv8Write p) {
   const float old = o0 > 0 ? *sp : 0.0f;  // read before thread 0 writes it, below the barrier
   if (NR > 0) {
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      float f[8];
-      v[i].floats(f);
-      m = amax_bits8(f, m);
-    }
+    for (int i = 0; i < NR; ++i) top.add(v[i]);
   } else {
     for (int run = o0 * RPT + threadIdx.x; run < o1 * RPT; run += blockDim.x) {
-      float f[8];
       v[0].load(src + (run / RPT) * ld + (run % RPT) * 8);
-      v[0].floats(f);
-      m = amax_bits8(f, m);
+      top.add(v[0]);
     }
   }
-  m = __reduce_max_sync(0xffffffffu, m);
+  uint32_t m = __reduce_max_sync(0xffffffffu, top.bits());
   if (lane == 0) red[threadIdx.x >> 5] = m;
   __syncthreads();
   m = red[lane % (blockDim.x / 32)];

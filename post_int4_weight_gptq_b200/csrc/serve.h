@@ -138,17 +138,44 @@ __device__ __forceinline__ float inverse_of(float scale) {
   return scale > 0.0f ? __frcp_rn(scale) : 0.0f;
 }
 
-// rint(x) for |x| < 2^22, in the low byte: adding 1.5 * 2^23 leaves the integer,
-// rounded to nearest even, in the low bits of the sum (two's complement).
+// The largest magnitude of many runs of eight.  16-bit types are compared two at a
+// time as integers.
+template <typename T>
+struct Largest {
+  uint32_t v = 0;
+  __device__ __forceinline__ void add(const Eight<T>& e) {
+#pragma unroll
+    for (int i = 0; i < Eight<T>::kVecs; ++i) {
+      const uint32_t w[4] = {e.v[i].x, e.v[i].y, e.v[i].z, e.v[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v = sizeof(T) == 2 ? __vmaxu2(v, w[j] & 0x7FFF7FFFu) : max(v, w[j] & 0x7FFFFFFFu);
+    }
+  }
+  __device__ __forceinline__ uint32_t bits() const;  // of the fp32 value
+};
+template <>
+__device__ __forceinline__ uint32_t Largest<float>::bits() const { return v; }
+template <>
+__device__ __forceinline__ uint32_t Largest<__nv_bfloat16>::bits() const {
+  return max(v & 0xFFFFu, v >> 16) << 16;
+}
+template <>
+__device__ __forceinline__ uint32_t Largest<__half>::bits() const {
+  const uint32_t m = max(v & 0xFFFFu, v >> 16);
+  return abs_bits(__half2float(__ushort_as_half(static_cast<unsigned short>(m))));
+}
+
+// rint(x * inverse) for |x| <= amax, in the low byte of each word: the product is
+// at most 127 (1 + 2^-22), which needs no clipping, and adding 1.5 * 2^23 leaves the
+// integer, rounded to nearest even, in the low bits of the sum (two's complement).
 __device__ __forceinline__ uint32_t code_bits(float x, float inverse) {
-  const float q = fminf(fmaxf(__fmul_rn(x, inverse), -127.0f), 127.0f);
-  return __float_as_uint(__fadd_rn(q, 12582912.0f));
+  return __float_as_uint(__fadd_rn(__fmul_rn(x, inverse), 12582912.0f));
 }
 __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
-// A non-finite x meets inverse 0 only: its product is NaN, and fmaxf drops the
-// NaN for -127, so the zero codes of such a set are made here.
+// A non-finite x meets inverse 0 only, where every code is 0.
 __device__ __forceinline__ uint2 codes8(const float (&f)[8], float inverse) {
   if (inverse == 0.0f) return make_uint2(0u, 0u);
   uint32_t c[8];
