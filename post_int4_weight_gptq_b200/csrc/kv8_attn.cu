@@ -45,20 +45,34 @@ constexpr int kWarps = 6;
 constexpr int kRing = 16 * 1024;      // bytes a warp: 2 stages of 32 keys and values of 128 dimensions
 constexpr int kMaxPages = 256;        // pages of a chunk (4096 keys, blocks of 16)
 
-// Bytes 0 and 2, and 1 and 3, of four codes, as halves.
-__device__ __forceinline__ void halves_of(uint32_t w, uint32_t& even, uint32_t& odd) {
+// Bytes 0 and 2, and 1 and 3, of four codes, as halves (low = 0x00FF00FF).
+__device__ __forceinline__ void halves_of(uint32_t w, uint32_t low, uint32_t& even, uint32_t& odd) {
   const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-  const uint32_t e = (w & 0x00FF00FFu) ^ 0x64806480u;
-  const uint32_t o = ((w >> 8) & 0x00FF00FFu) ^ 0x64806480u;
+  const uint32_t e = (w & low) ^ 0x64806480u;
+  const uint32_t o = ((w >> 8) & low) ^ 0x64806480u;
   const __half2 eh = __hsub2(*reinterpret_cast<const __half2*>(&e), off);
   const __half2 oh = __hsub2(*reinterpret_cast<const __half2*>(&o), off);
   even = *reinterpret_cast<const uint32_t*>(&eh);
   odd = *reinterpret_cast<const uint32_t*>(&oh);
 }
 // The same, each + 128 and times 2^-24.
-__device__ __forceinline__ void biased_halves_of(uint32_t w, uint32_t& even, uint32_t& odd) {
-  even = (w & 0x00FF00FFu) ^ 0x00800080u;
-  odd = ((w >> 8) & 0x00FF00FFu) ^ 0x00800080u;
+__device__ __forceinline__ void biased_halves_of(uint32_t w, uint32_t low, uint32_t& even,
+                                                 uint32_t& odd) {
+  even = (w & low) ^ 0x00800080u;
+  odd = ((w >> 8) & low) ^ 0x00800080u;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -283,13 +297,15 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
   }
 
   int stage = 0;
+  const uint32_t mine_at = smem_u32(mine), low = p.low_bytes;
+  float per_vmax = 0.0f;  // kPScale / vmax
   uint32_t phase = 0;
   bool ok = true;
   // One step; MASK: some row does not see all of its keys.  Two forms, because the
   // compiler would turn a branch around the masks into selects on every step.
   auto process = [&](int step, auto mask_c) {
     constexpr bool MASK = decltype(mask_c)::value;
-    const uint8_t* const at = mine + stage * STAGE;
+    const uint32_t at = mine_at + stage * STAGE;
     const int key0 = 32 * step;
     float s[2][NT][4] = {}, kscale[2], vscale[2];
 #pragma unroll
@@ -303,15 +319,14 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
     for (int j = 0; j < KV; ++j)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const uint8_t* a = at + u * (16 * D) + (k_at ^ (64 * j));
-        const uint4 w0 = *reinterpret_cast<const uint4*>(a);
-        const uint4 w1 = *reinterpret_cast<const uint4*>(a + 8 * D);
+        const uint4 w0 = lds128(at + (k_at ^ (64 * j)) + u * (16 * D));
+        const uint4 w1 = lds128(at + (k_at ^ (64 * j)) + u * (16 * D) + 8 * D);
         const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           uint32_t a0, a1, a2, a3;
-          biased_halves_of(x0[w], a0, a2);
-          biased_halves_of(x1[w], a1, a3);
+          biased_halves_of(x0[w], low, a0, a2);
+          biased_halves_of(x1[w], low, a1, a3);
 #pragma unroll
           for (int t = 0; t < NT; ++t)
             mma_f16(s[u][t], a0, a1, a2, a3, qf[t][4 * j + w][0], qf[t][4 * j + w][1]);
@@ -348,6 +363,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
       const float fresh = fmaxf(fmaxf(vscale[0], vscale[1]), vmax);
       const float fv = vmax > 0.0f ? vmax / fresh : 0.0f;
       vmax = fresh;
+      per_vmax = vmax > 0.0f ? kPScale / vmax : 0.0f;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         float f[2];
@@ -377,8 +393,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
     uint32_t pb[2][NT][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const float vf = vmax > 0.0f ? __fdividef(kPScale * vscale[u], vmax)
-                                   : (vscale[u] == vscale[u] ? 0.0f : vscale[u]);
+      const float vf = vscale[u] * per_vmax;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -402,15 +417,15 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
       uint32_t vr[4][D / 32];
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
-        const uint8_t* a = at + u * (16 * D) + v_at[h & 1] + (h >> 1) * (8 * D);
+        const uint32_t a = at + v_at[h & 1] + u * (16 * D) + (h >> 1) * (8 * D);
         if constexpr (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(a);
+          const uint4 x = lds128(a);
           vr[h][0] = x.x;
           vr[h][1] = x.y;
           vr[h][2] = x.z;
           vr[h][3] = x.w;
         } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(a);
+          const uint2 x = lds64(a);
           vr[h][0] = x.x;
           vr[h][1] = x.y;
         }
@@ -422,8 +437,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel
         for (int half = 0; half < 2; ++half) {
           const uint32_t sel = half == 0 ? 0x5410u : 0x7632u;  // d0 d1 | d2 d3 of both tokens
           uint32_t a0, a1, a2, a3;
-          halves_of(__byte_perm(vr[0][w], vr[1][w], sel), a0, a1);
-          halves_of(__byte_perm(vr[2][w], vr[3][w], sel), a2, a3);
+          halves_of(__byte_perm(vr[0][w], vr[1][w], sel), low, a0, a1);
+          halves_of(__byte_perm(vr[2][w], vr[3][w], sel), low, a2, a3);
 #pragma unroll
           for (int t = 0; t < NT; ++t)
             mma_f16(o[t][2 * w + half], a0, a1, a2, a3, pb[u][t][0], pb[u][t][1]);

@@ -27,6 +27,8 @@ struct Kv8Attn {
   float* part_o;   // [chunks][tokens][heads][D] when chunks > 1
   float2* part_ml; // [chunks][tokens][heads]: running maximum (log2), sum
   int32_t* status;
+  uint32_t low_bytes = 0x00FF00FFu;  // a parameter, so that (w & mask) ^ constant is one
+                                     // instruction: with two literals it became two
 };
 
 constexpr float kLn2 = 0.6931471805599453f;
