@@ -63,9 +63,9 @@ __device__ __forceinline__ void tmem_st_wait() {
 }
 
 // A warpgroup's registers a thread.  The block is launched with 16 warps of 128
-// registers; the shares below (2 x 136 softmax, 168 widening, 64 the rest) stay
-// within that.
-constexpr int kRegSoftmax = 136, kRegWiden = 168, kRegIssue = 64;
+// registers; the shares below (2 x 168 softmax, 120 widening, 56 the rest) are all
+// of that.
+constexpr int kRegSoftmax = 168, kRegWiden = 120, kRegIssue = 56;
 static_assert(2 * kRegSoftmax + kRegWiden + kRegIssue <= 4 * 128, "more than the launch has");
 template <int N>
 __device__ __forceinline__ void more_registers() {
@@ -117,10 +117,9 @@ __device__ __forceinline__ uint32_t seen(int from, int upto, int c) {
   return a == 32 ? 0u : below & ~((1u << a) - 1u);
 }
 
-// The largest of a row's 128 scores (scaled), this thread's TMEM lane at ts.
-// MASK: only keys [from, upto) count.  Kept apart from the unmasked form, which
-// all but a few tiles take: selects for every key cost as much as the rest.
-template <bool MASK>
+// The largest of a row's 128 scores (scaled), this thread's TMEM lane at ts, of the
+// keys [from, upto).  Kept apart from the unmasked form, which all but a few tiles
+// take: selects for every key cost as much as the rest.
 __device__ __forceinline__ float row_max(uint32_t ts, float rs, const float* ks, int from,
                                          int upto) {
   const float ninf = __uint_as_float(0xFF800000u);
@@ -129,11 +128,9 @@ __device__ __forceinline__ float row_max(uint32_t ts, float rs, const float* ks,
   for (int c = 0; c < KT / 32; ++c) {
     float s[32];
     tmem_ld_32x32b_x32(ts + 32 * c, s);
-    if (MASK) {
-      const uint32_t bits = seen(from, upto, c);
+    const uint32_t bits = seen(from, upto, c);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) s[i] = (bits >> i) & 1u ? s[i] : ninf;
-    }
+    for (int i = 0; i < 32; ++i) s[i] = (bits >> i) & 1u ? s[i] : ninf;
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       // a score times the (positive) scales is monotone in it
@@ -151,7 +148,6 @@ __device__ __forceinline__ float row_max(uint32_t ts, float rs, const float* ks,
 
 // The row's probabilities relative to m, summed into l2, and times the blocks'
 // value factors as halves over the scores.
-template <bool MASK>
 __device__ __forceinline__ void row_weights(uint32_t ts, float rs, float m, const float* ks,
                                             const float* vfs, int from, int upto, uint64_t& l2) {
   const float ninf = __uint_as_float(0xFF800000u);
@@ -161,7 +157,7 @@ __device__ __forceinline__ void row_weights(uint32_t ts, float rs, float m, cons
     float s[32];
     uint32_t w[16];
     tmem_ld_32x32b_x32(ts + 32 * c, s);
-    const uint32_t bits = MASK ? seen(from, upto, c) : 0xFFFFFFFFu;
+    const uint32_t bits = seen(from, upto, c);
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       const float f = rs * ks[2 * c + g], vf = vfs[2 * c + g];
@@ -170,17 +166,14 @@ __device__ __forceinline__ void row_weights(uint32_t ts, float rs, float m, cons
       for (int i = 16 * g; i < 16 * g + 16; i += 2) {
         float x0, x1, y0, y1;
         unpack2(fma2(pack2(s[i], s[i + 1]), f2, nm2), x0, x1);
-        if (MASK) {
-          x0 = (bits >> i) & 1u ? x0 : ninf;
-          x1 = (bits >> (i + 1)) & 1u ? x1 : ninf;
-        }
+        x0 = (bits >> i) & 1u ? x0 : ninf;
+        x1 = (bits >> (i + 1)) & 1u ? x1 : ninf;
         const uint64_t e = pack2(exp2_fast(x0), exp2_fast(x1));
         l2 = add2(l2, e);
         unpack2(mul2(e, vf2), y0, y1);
-        if (MASK) {  // 0 times the scale of a block that holds a NaN is not 0
-          y0 = (bits >> i) & 1u ? y0 : 0.0f;
-          y1 = (bits >> (i + 1)) & 1u ? y1 : 0.0f;
-        }
+        // 0 times the scale of a block that holds a NaN is not 0
+        y0 = (bits >> i) & 1u ? y0 : 0.0f;
+        y1 = (bits >> (i + 1)) & 1u ? y1 : 0.0f;
         const __half2 h = __floats2half2_rn(y0, y1);
         w[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
       }
@@ -193,6 +186,84 @@ __device__ __forceinline__ void row_weights(uint32_t ts, float rs, float m, cons
 // 128 rows: halves of 64 dimensions, 128-byte rows, 128-byte swizzle.
 __device__ __forceinline__ uint32_t tile_at(int row, int piece) {
   return (piece >> 3) * (KT * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+}
+
+// 32 columns of this warp's lanes; the values are there after tmem_ld_done, which
+// also keeps their uses behind the wait.
+__device__ __forceinline__ void tmem_ld_start(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[32]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                 "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
+                 "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
+                 "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+
+// A row of scores held in registers from one read of tensor memory, for tiles that
+// need no masks: their largest (scaled), and behind that the same as row_weights.
+// (Reading them twice, 32 at a time, left the warp waiting for tensor memory eight
+// times a tile: 277 us instead of %%PLACE%%.)
+__device__ __forceinline__ float held_max(const uint32_t (&s)[4][32], float rs, const float* ks) {
+  float top = __uint_as_float(0xFF800000u);
+#pragma unroll
+  for (int g = 0; g < kGran; ++g) {
+    const uint32_t* v = s[g / 2] + 16 * (g & 1);
+    float x = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
+    float y = fmaxf(__uint_as_float(v[2]), __uint_as_float(v[3]));
+#pragma unroll
+    for (int i = 4; i < 16; i += 4) {
+      x = fmaxf(fmaxf(x, __uint_as_float(v[i])), __uint_as_float(v[i + 1]));
+      y = fmaxf(fmaxf(y, __uint_as_float(v[i + 2])), __uint_as_float(v[i + 3]));
+    }
+    top = fmaxf(top, fmaxf(x, y) * (rs * ks[g]));
+  }
+  return top;
+}
+__device__ __forceinline__ void held_weights(const uint32_t (&s)[4][32], uint32_t ts, float rs,
+                                             float m, const float* ks, const float* vfs,
+                                             uint64_t& l2) {
+  const uint64_t nm2 = pack2(-m, -m);
+  uint64_t la = 0, lb = 0;  // two chains of the sum
+#pragma unroll
+  for (int c = 0; c < KT / 32; ++c) {
+    uint32_t w[16];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const float f = rs * ks[2 * c + g], vf = vfs[2 * c + g];
+      const uint64_t f2 = pack2(f, f), vf2 = pack2(vf, vf);
+#pragma unroll
+      for (int i = 16 * g; i < 16 * g + 16; i += 2) {
+        float x0, x1, y0, y1;
+        unpack2(fma2(pack2(__uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1])), f2, nm2), x0,
+                x1);
+        const uint64_t e = pack2(exp2_fast(x0), exp2_fast(x1));
+        if (i & 2)
+          la = add2(la, e);
+        else
+          lb = add2(lb, e);
+        unpack2(mul2(e, vf2), y0, y1);
+        const __half2 h = __floats2half2_rn(y0, y1);
+        w[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    tmem_st_x16(ts + 16 * c, w);
+  }
+  l2 = add2(l2, add2(la, lb));
 }
 
 // Row `row` of a query tile from src (zeros for nullptr), as halves; returns the
@@ -399,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
     }
   } else if (warp >= 8) {
     // ------------------------------------------------ widening keys and values
-    more_registers<kRegWiden>();
+    fewer_registers<kRegWiden>();
     // A granule of 16 keys is one run of 16 D bytes; the 128 threads take 128 / D
     // of them at a time, 16 bytes each.  Four lanes share a key's 64 dimensions and
     // the next four the key after it, whose swizzle puts their halves into the other
@@ -516,31 +587,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
         // keys [from, to) of the tile are seen
         const int from = max(lo - key0, 0), upto = min(max(hi - key0, 0), KT);
         const bool mask = __any_sync(0xffffffffu, from > 0 || upto < KT);
-        const float top = mask ? row_max<true>(ts, rs, sh.ks[slot], from, upto)
-                               : row_max<false>(ts, rs, sh.ks[slot], from, upto);
-        if (__any_sync(0xffffffffu, top > m + kSlack)) {
+        // The running maximum moves (and O is rescaled) when a score passes it by 2^8.
+        auto move = [&](float top) {
+          if (!__any_sync(0xffffffffu, top > m + kSlack)) return true;
           const float nm = fmaxf(m, top);
           const float f = exp2_fast(m - nm);
           m = nm;
           l2 = mul2(l2, pack2(f, f));
-          if (j > 0) {
-            if (!(ok = wait_warp(&sh.pv_done[t], (j - 1) & 1, p.status, 79))) break;
-            tc_fence_after();
+          if (j == 0) return true;
+          if (!wait_warp(&sh.pv_done[t], (j - 1) & 1, p.status, 79)) return false;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            float o[16];
+            uint32_t w[16];
+            tmem_ld_32x32b_x16(to + 16 * c, o);
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-              float o[16];
-              uint32_t w[16];
-              tmem_ld_32x32b_x16(to + 16 * c, o);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * f);
-              tmem_st_x16(to + 16 * c, w);
-            }
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * f);
+            tmem_st_x16(to + 16 * c, w);
           }
+          return true;
+        };
+        if (mask) {
+          if (!(ok = move(row_max(ts, rs, sh.ks[slot], from, upto)))) break;
+          row_weights(ts, rs, m, sh.ks[slot], sh.vf[slot], from, upto, l2);
+        } else {
+          uint32_t s[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld_start(ts + 32 * c, s[c]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld_done(s[c]);
+          if (!(ok = move(held_max(s, rs, sh.ks[slot])))) break;
+          held_weights(s, ts, rs, m, sh.ks[slot], sh.vf[slot], l2);
         }
-        if (mask)
-          row_weights<true>(ts, rs, m, sh.ks[slot], sh.vf[slot], from, upto, l2);
-        else
-          row_weights<false>(ts, rs, m, sh.ks[slot], sh.vf[slot], from, upto, l2);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
