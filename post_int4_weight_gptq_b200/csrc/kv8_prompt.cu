@@ -17,10 +17,8 @@
 //
 // 16 warps: 0 - 3 and 4 - 7 the softmax of tile 0 and 1 (a row a thread),
 // 8 - 11 widen keys and values, 12 issues the MMAs (13 - 15 only give their
-// registers away).  The two tiles alternate: one
-// tile's softmax runs while the tensor cores work for the other.  The MMAs of a
-// CTA execute in the order they are issued, so the scores of the next keys may be
-// issued over the P that the product before them reads.  Every wait is bounded.
+// registers away).  The two tiles alternate: one tile's softmax runs while the tensor
+// cores work for the other.  Every wait is bounded.
 #include <algorithm>
 #include <atomic>
 
@@ -63,9 +61,9 @@ __device__ __forceinline__ void tmem_st_wait() {
 }
 
 // A warpgroup's registers a thread.  The block is launched with 16 warps of 128
-// registers; the shares below (2 x 168 softmax, 120 widening, 56 the rest) are all
+// registers; the shares below (2 x 144 softmax, 152 widening, 72 the rest) are all
 // of that.
-constexpr int kRegSoftmax = 168, kRegWiden = 120, kRegIssue = 56;
+constexpr int kRegSoftmax = 144, kRegWiden = 152, kRegIssue = 72;
 static_assert(2 * kRegSoftmax + kRegWiden + kRegIssue <= 4 * 128, "more than the launch has");
 template <int N>
 __device__ __forceinline__ void more_registers() {
@@ -214,15 +212,15 @@ __device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[32]) {
                  "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
 
-// A row of scores held in registers from one read of tensor memory, for tiles that
-// need no masks: their largest (scaled), and behind that the same as row_weights.
-// (Reading them twice, 32 at a time, left the warp waiting for tensor memory eight
-// times a tile: 277 us instead of %%PLACE%%.)
-__device__ __forceinline__ float held_max(const uint32_t (&s)[4][32], float rs, const float* ks) {
-  float top = __uint_as_float(0xFF800000u);
+// The unmasked forms of the two, 32 columns at a time: their largest score, and their
+// probabilities relative to m as halves in w.  (All 128 columns in registers from one
+// read, unrolled, came out slower: 315 us, the code no longer fits the instruction
+// cache beside the other roles'.)
+__device__ __forceinline__ float part_max(const uint32_t (&s)[32], float rs, const float* ks,
+                                          float top) {
 #pragma unroll
-  for (int g = 0; g < kGran; ++g) {
-    const uint32_t* v = s[g / 2] + 16 * (g & 1);
+  for (int g = 0; g < 2; ++g) {
+    const uint32_t* v = s + 16 * g;
     float x = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
     float y = fmaxf(__uint_as_float(v[2]), __uint_as_float(v[3]));
 #pragma unroll
@@ -234,64 +232,64 @@ __device__ __forceinline__ float held_max(const uint32_t (&s)[4][32], float rs, 
   }
   return top;
 }
-__device__ __forceinline__ void held_weights(const uint32_t (&s)[4][32], uint32_t ts, float rs,
-                                             float m, const float* ks, const float* vfs,
-                                             uint64_t& l2) {
-  const uint64_t nm2 = pack2(-m, -m);
-  uint64_t la = 0, lb = 0;  // two chains of the sum
+__device__ __forceinline__ void part_weights(const uint32_t (&s)[32], uint32_t to, float rs,
+                                             uint64_t nm2, const float* ks, const float* vfs,
+                                             uint64_t& la, uint64_t& lb) {
+  uint32_t w[16];
 #pragma unroll
-  for (int c = 0; c < KT / 32; ++c) {
-    uint32_t w[16];
+  for (int g = 0; g < 2; ++g) {
+    const float f = rs * ks[g], vf = vfs[g];
+    const uint64_t f2 = pack2(f, f), vf2 = pack2(vf, vf);
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const float f = rs * ks[2 * c + g], vf = vfs[2 * c + g];
-      const uint64_t f2 = pack2(f, f), vf2 = pack2(vf, vf);
-#pragma unroll
-      for (int i = 16 * g; i < 16 * g + 16; i += 2) {
-        float x0, x1, y0, y1;
-        unpack2(fma2(pack2(__uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1])), f2, nm2), x0,
-                x1);
-        const uint64_t e = pack2(exp2_fast(x0), exp2_fast(x1));
-        if (i & 2)
-          la = add2(la, e);
-        else
-          lb = add2(lb, e);
-        unpack2(mul2(e, vf2), y0, y1);
-        const __half2 h = __floats2half2_rn(y0, y1);
-        w[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
-      }
+    for (int i = 16 * g; i < 16 * g + 16; i += 2) {
+      float x0, x1, y0, y1;
+      unpack2(fma2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), f2, nm2), x0, x1);
+      const uint64_t e = pack2(exp2_fast(x0), exp2_fast(x1));
+      if (i & 2)
+        la = add2(la, e);
+      else
+        lb = add2(lb, e);
+      unpack2(mul2(e, vf2), y0, y1);
+      const __half2 h = __floats2half2_rn(y0, y1);
+      w[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    tmem_st_x16(ts + 16 * c, w);
   }
-  l2 = add2(l2, add2(la, lb));
+  tmem_st_x16(to, w);
 }
 
-// Row `row` of a query tile from src (zeros for nullptr), as halves; returns the
-// positive factor of its scores (log2 units), the sign of scale2 going into the
-// halves.  A row that holds an infinity or NaN is zeros under a NaN factor.
+// The 32 query rows of a warp (row0 of `rows`, row `at` of the tile) to halves in
+// shared memory.  Lanes go along a row, so that a load meets two or four rows' bytes
+// whole (a row a lane took 5 us); every lane then takes its own row's factor: the
+// positive factor of its scores in log2 units (the sign of scale2 goes into the
+// halves).  A row that holds an infinity or NaN is zeros under a NaN factor.
 template <typename T, int D>
-__device__ __forceinline__ float stage_query(const T* src, uint8_t* tile, int row, float scale2) {
-  Eight<T> v[D / 8];
-  uint32_t m = 0;
+__device__ __forceinline__ float stage_queries(const Kv8Attn& p, int64_t q0, int kvh, int row0,
+                                               int rows, uint8_t* tile, int at, int lane) {
+  constexpr int LPR = D / 8, RPL = 32 / LPR;  // lanes a row, rows a load
+  Eight<T> v[LPR];
+  const int piece = lane % LPR, sub = lane / LPR;
+  int tok = static_cast<int>(static_cast<unsigned>(row0 + sub) / p.group);
+  int head = row0 + sub - tok * p.group;  // stepped below: a division a row is slow
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
-    if (src != nullptr)
-      v[i].load(src + 8 * i);
-    else
-      v[i].zero();
+  for (int i = 0; i < LPR; ++i) {
+    v[i].zero();
+    if (row0 + i * RPL + sub < rows)
+      v[i].load(static_cast<const T*>(p.q) + (q0 + tok) * p.ldq + (kvh * p.group + head) * D +
+                8 * piece);
+    for (head += RPL; head >= p.group; head -= p.group) ++tok;
   }
+  float mine = 0.0f;
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
-    float f[8];
-    v[i].floats(f);
-    m = amax_bits8(f, m);
-  }
-  float mul;
-  const float undo = row_exponent<T>(__uint_as_float(m), mul);
-  const bool fine = undo == undo;
-  if (scale2 < 0.0f) mul = -mul;
+  for (int i = 0; i < LPR; ++i) {
+    Largest<T> top;
+    top.add(v[i]);
+    uint32_t m = top.bits();
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
+    for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float mul;
+    const float undo = row_exponent<T>(__uint_as_float(m), mul);
+    const bool fine = undo == undo;
+    if (p.scale2 < 0.0f) mul = -mul;
     float f[8];
     uint32_t w[4];
     v[i].floats(f);
@@ -300,9 +298,14 @@ __device__ __forceinline__ float stage_query(const T* src, uint8_t* tile, int ro
       const __half2 h = __floats2half2_rn(f[2 * j] * mul, f[2 * j + 1] * mul);
       w[j] = fine ? *reinterpret_cast<const uint32_t*>(&h) : 0u;
     }
-    *reinterpret_cast<uint4*>(tile + tile_at(row, i)) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(tile + tile_at(at + i * RPL + sub, piece)) =
+        make_uint4(w[0], w[1], w[2], w[3]);
+    const float rs = undo * fabsf(p.scale2);
+    // row i RPL + s of the warp is lane i RPL + s's, and lanes s LPR .. have its factor
+    const float got = __shfl_sync(0xffffffffu, rs, (lane % RPL) * LPR);
+    if (lane / RPL == i) mine = got;
   }
-  return undo * fabsf(scale2);
+  return mine;
 }
 
 template <int D>
@@ -314,7 +317,7 @@ struct Layout {
 
 struct Shared {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2];
-  uint64_t sc_full[4], q_full;
+  uint64_t sc_full[4], q_full, o_done;
   float ks[4][kGran], vf[4][kGran];  // scales of a tile: a ring of four, so that a slot is
                                      // rewritten only after both softmaxes have left it
   int vmax;
@@ -397,6 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
     }
     for (int i = 0; i < 4; ++i) mbar_init(&sh.sc_full[i], 1);
     mbar_init(&sh.q_full, 4 * nq);
+    mbar_init(&sh.o_done, 1);
     sh.vmax = 0;
     fence_mbar_init();
   }
@@ -459,18 +463,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
                         smem_desc(v + kk * 2048, KT * 128, 1024, kLayoutSw128), id_o,
                         (j | kk) != 0);
           umma_commit(&sh.pv_done[t]);
-          if (more) scores(t, st ^ 1);
+          if (more) {
+            // The next scores go over the P that this product reads: MMAs on other
+            // accumulators are not ordered behind it, so its end is waited for.
+            if (!(ok = wait_bar(&sh.pv_done[t], j & 1, p.status, 76))) break;
+            scores(t, st ^ 1);
+          }
         }
         if (!ok) break;
         umma_commit(&sh.v_empty[st]);
         if (more) umma_commit(&sh.k_empty[st ^ 1]);
       }
-      // the last arrival is in before the barriers' memory goes
-      if (ok) wait_bar(&sh.v_empty[(nt - 1) & 1], ((nt - 1) >> 1) & 1, p.status, 81);
+      // the end of everything; the arrival is in before the barrier's memory goes
+      if (ok) {
+        umma_commit(&sh.o_done);
+        wait_bar(&sh.o_done, 0, p.status, 81);
+      }
     }
   } else if (warp >= 8) {
     // ------------------------------------------------ widening keys and values
-    fewer_registers<kRegWiden>();
+    more_registers<kRegWiden>();
     // A granule of 16 keys is one run of 16 D bytes; the 128 threads take 128 / D
     // of them at a time, 16 bytes each.  Four lanes share a key's 64 dimensions and
     // the next four the key after it, whose swizzle puts their halves into the other
@@ -534,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
       const float tks = gks, tvs = gvs;
       look(j + 1);
       fetch(j + 2);
-      if (!wait_warp(&sh.k_empty[st], ((j >> 1) & 1) ^ 1u, p.status, 75)) break;
+      if (!wait_warp(&sh.k_empty[st], ((j >> 1) & 1) ^ 1u, p.status, 83)) break;
       if (warp == 8) {
         if (lane < kGran) {
           sh.ks[slot][lane] = tks;
@@ -548,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.k_full[st]);
       if (j + 1 < nt) load(p.kc, kr);
-      if (!wait_warp(&sh.v_empty[st], ((j >> 1) & 1) ^ 1u, p.status, 76)) break;
+      if (!wait_warp(&sh.v_empty[st], ((j >> 1) & 1) ^ 1u, p.status, 84)) break;
       store(smem + L::V_AT + st * L::TILE, vr);
       fence_proxy_async_smem();
       __syncwarp();
@@ -564,9 +576,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
       const unsigned rel = (live ? row : 0u) / p.group;
       const int64_t tok = q0 + rel;
       const int head = kvh * p.group + static_cast<int>((live ? row : 0u) - rel * p.group);
-      const float rs = stage_query<T, D>(
-          live ? static_cast<const T*>(p.q) + tok * p.ldq + head * D : nullptr,
-          smem + (threadIdx.x >> 7) * L::TILE, threadIdx.x & 127, p.scale2);
+      const float rs = stage_queries<T, D>(p, q0, kvh, row0 + 32 * warp, rows,
+                                           smem + (warp >> 2) * L::TILE, 32 * (warp & 3), lane);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_full);
@@ -608,18 +619,43 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
           }
           return true;
         };
+        const float *ks = sh.ks[slot], *vf = sh.vf[slot];
         if (mask) {
-          if (!(ok = move(row_max(ts, rs, sh.ks[slot], from, upto)))) break;
-          row_weights(ts, rs, m, sh.ks[slot], sh.vf[slot], from, upto, l2);
+          if (!(ok = move(row_max(ts, rs, ks, from, upto)))) break;
+          row_weights(ts, rs, m, ks, vf, from, upto, l2);
         } else {
-          uint32_t s[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld_start(ts + 32 * c, s[c]);
+          // two buffers of 32 columns: one is on its way while the other is worked on
+          uint32_t sa[32], sb[32];
+          float top = __uint_as_float(0xFF800000u);
+          tmem_ld_start(ts, sa);
+#pragma unroll 1
+          for (int c = 0; c < 4; c += 2) {
+            tmem_ld_wait();
+            tmem_ld_done(sa);
+            tmem_ld_start(ts + 32 * (c + 1), sb);
+            top = part_max(sa, rs, ks + 2 * c, top);
+            tmem_ld_wait();
+            tmem_ld_done(sb);
+            tmem_ld_start(ts + 32 * ((c + 2) & 3), sa);  // at last the first ones again
+            top = part_max(sb, rs, ks + 2 * c + 2, top);
+          }
           tmem_ld_wait();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld_done(s[c]);
-          if (!(ok = move(held_max(s, rs, sh.ks[slot])))) break;
-          held_weights(s, ts, rs, m, sh.ks[slot], sh.vf[slot], l2);
+          tmem_ld_done(sa);
+          if (!(ok = move(top))) break;
+          const uint64_t nm2 = pack2(-m, -m);
+          uint64_t lb = 0;
+#pragma unroll 1
+          for (int c = 0; c < 4; c += 2) {
+            tmem_ld_start(ts + 32 * (c + 1), sb);
+            part_weights(sa, ts + 16 * c, rs, nm2, ks + 2 * c, vf + 2 * c, l2, lb);
+            tmem_ld_wait();
+            tmem_ld_done(sb);
+            if (c == 0) tmem_ld_start(ts + 64, sa);
+            part_weights(sb, ts + 16 * c + 16, rs, nm2, ks + 2 * c + 2, vf + 2 * c + 2, l2, lb);
+            tmem_ld_wait();
+            tmem_ld_done(sa);
+          }
+          l2 = add2(l2, lb);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -627,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
         if (lane == 0) mbar_arrive(&sh.p_full[t]);
       }
       // ------------------------------------------------------------------- result
-      if (ok && nt > 0) ok = wait_warp(&sh.pv_done[t], (nt - 1) & 1, p.status, 80);
+      if (ok && nt > 0) ok = wait_warp(&sh.o_done, 0, p.status, 80);
       tc_fence_after();
       const float vmax = __int_as_float(sh.vmax);
       float la, lb;

@@ -31,14 +31,28 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn tensor_map_encoder();
 
-// A bounded wait (mbar_wait) that reports to the caller's status words.
+// A bounded wait that reports to the caller's status words.  Without mbar_wait's
+// suspend hint: these kernels' roles wait for one another several times a microsecond,
+// and waking from the hinted sleep took hundreds of cycles each time.
 __device__ __forceinline__ void note_status(int32_t* status, int code, int detail);
+__device__ __forceinline__ bool try_wait_now(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int32_t* status,
                                          int where) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (try_wait_now(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   for (;;) {
-    if (mbar_try_wait(bar, parity)) return true;
+    for (int i = 0; i < 64; ++i)
+      if (try_wait_now(bar, parity)) return true;
     if (global_timer_ns() - t0 > kWaitLimitNs) {
       note_status(status, PIQ_ERR_TIMEOUT, where);
       return false;
@@ -120,12 +134,6 @@ __device__ __forceinline__ __half from_float<__half>(float x) { return __float2h
 // Largest magnitude as a bit pattern: ordered like the values, and an infinity
 // or NaN is larger than every finite one.
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
-
-__device__ __forceinline__ uint32_t amax_bits8(const float (&f)[8], uint32_t m) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, abs_bits(f[i]));
-  return m;
-}
 
 // scale = amax / 127 (0 below 2^-126, NaN for an infinity or NaN).
 __device__ __forceinline__ float scale_of(uint32_t amax_bits) {

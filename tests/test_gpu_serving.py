@@ -377,6 +377,34 @@ def test_attention_split_and_joined(max_len, news, window):
     check_attention(b, q, news, *run_attention(b, q, news, max_len, window), window=window)
 
 
+@pytest.mark.parametrize("dtype,heads,kv_heads,dim,block,news,lens,window", [
+    (BF16, 4, 1, 128, 16, [300], [1500], 0), (BF16, 8, 4, 64, 128, [260, 90], [700, 1300], 0),
+    (FP16, 2, 2, 128, 64, [513], [513], 0), (BF16, 16, 2, 128, 32, [40, 3, 200], [900, 2000, 210], 333),
+    (FP16, 64, 2, 64, 64, [20, 9], [1100, 70], 0)])
+def test_attention_prompts(dtype, heads, kv_heads, dim, block, news, lens, window):
+    # several tiles of rows and of keys, scales that move between blocks
+    rng = np.random.default_rng(heads * block)
+    b = Batch(rng, lens, kv_heads, dim, block, dtype)
+    half = [(a - n) // 2 for a, n in zip(lens, news)]
+    b.append(half, std=0.2)
+    b.append([a - n - h for a, n, h in zip(lens, news, half)], std=3.0)
+    b.append(news)
+    q = rand(rng, (sum(news), heads, dim), dtype, 1.5)
+    check_attention(b, q, news, *run_attention(b, q, news, window=window), window=window)
+    big = max(lens) * 40          # a bound that splits the keys of few rows
+    check_attention(b, q, news, *run_attention(b, q, news, big, window), window=window)
+
+
+def test_attention_negative_scale():
+    rng = np.random.default_rng(17)
+    b = Batch(rng, [200, 90], 2, 64, 32, BF16)
+    b.append([190, 30])
+    for news in ([1, 1], [9, 59]):
+        b.append(news)
+        q = rand(rng, (sum(news), 8, 64), BF16)
+        check_attention(b, q, news, *run_attention(b, q, news, scale=-0.3), scale=-0.3)
+
+
 def test_attention_rows_and_strides():
     rng = np.random.default_rng(8)
     b = Batch(rng, [70, 9], 2, 64, 16, BF16)
