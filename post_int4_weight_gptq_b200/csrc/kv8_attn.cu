@@ -42,7 +42,11 @@ namespace piq {
 namespace {
 
 constexpr int kWarps = 6;
-constexpr int kRing = 16 * 1024;      // bytes a warp: 2 stages of 32 keys and values of 128 dimensions
+// Bytes of a warp's ring: two stages of 32 keys and values.
+constexpr int ring_bytes(int dim) { return 2 * 64 * dim; }
+// CTAs that share a multiprocessor, as their registers allow (three of 64 dimensions
+// and one group of rows instead of two: 70 -> 63 us on 48 ragged sequences).
+constexpr int ctas_sm(int dim, int nt) { return (dim == 64 ? 4 : 3) - nt; }
 constexpr int kMaxPages = 256;        // pages of a chunk (4096 keys, blocks of 16)
 
 // Bytes 0 and 2, and 1 and 3, of four codes, as halves (low = 0x00FF00FF).
@@ -104,13 +108,13 @@ __device__ __forceinline__ int token_of(int k) {
 // NT groups of eight query rows of one kv head (rows are (token, head) pairs,
 // the heads of the group fastest) against one chunk of keys.
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) kv8_chunk_kernel(
+__global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, Kv8Attn p) {
   constexpr int ROWS = 8 * NT;
   constexpr int KS = D / 16;   // k steps of the scores = 16-row tiles of the output
   constexpr int KV = D / 64;   // 16-byte loads of a key a lane; value loads are 4 of D / 8 bytes
   constexpr int STAGE = 64 * D;            // bytes of 32 keys, then their 32 values
-  constexpr int STAGES = kRing / STAGE;
+  constexpr int kRing = ring_bytes(D), STAGES = kRing / STAGE;
   __shared__ int s_page[kMaxPages];  // page kv_heads + head
   __shared__ float s_ks[kMaxPages], s_vs[kMaxPages];
   __shared__ __align__(16) __half s_q[ROWS][D];
@@ -609,7 +613,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv8_join_kernel(Kv8Attn p) {
         total == 0.0f ? __uint_as_float(0xFF800000u) : (top + log2f(total)) * kLn2;
 }
 
-// Keys a chunk: one wave of two CTAs a multiprocessor where the sequences and heads
+// Keys a chunk: one wave of CTAs where the sequences and heads
 // alone do not fill it, but no chunk so short that starting and joining it costs
 // more than it spreads; where they do, chunks that even out ragged lengths.
 constexpr int64_t kMinChunk = 256, kManyCtasChunk = 2048, kMaxChunk = 4096;
@@ -624,7 +628,7 @@ struct AttnPlan {
   int chunks;
 };
 
-AttnPlan plan_attention(int64_t tokens, int heads, int kv_heads, int64_t batch, int64_t max_new, int64_t max_len,
+AttnPlan plan_attention(int64_t tokens, int heads, int kv_heads, int head_dim, int64_t batch, int64_t max_new, int64_t max_len,
                         int64_t window) {
   AttnPlan a;
   a.window = window < max_len ? static_cast<int>(window) : 0;  // a wider one hides nothing
@@ -646,7 +650,7 @@ AttnPlan plan_attention(int64_t tokens, int heads, int kv_heads, int64_t batch, 
     return a;
   }
   const int64_t ctas = a.row_groups * kv_heads * batch;
-  const int64_t want = 2 * 148 / ctas;
+  const int64_t want = 148 * ctas_sm(head_dim, a.nt) / ctas;
   a.chunk = want > 1 ? ceil_div(ceil_div(span, want), 128) * 128 : kManyCtasChunk;
   a.chunk = std::min(std::max(a.chunk, kMinChunk), kMaxChunk);
   a.chunks = static_cast<int>(ceil_div(span, a.chunk));
@@ -708,7 +712,7 @@ int launch_attention(const Kv8Attn& p, const AttnPlan& a, cudaStream_t stream) {
   }
   void (*kern)(CUtensorMap, CUtensorMap, Kv8Attn) = a.nt == 1 ? kv8_chunk_kernel<T, D, 1> : kv8_chunk_kernel<T, D, 2>;
   const unsigned gx = static_cast<unsigned>(a.row_groups * p.kv_heads);
-  constexpr int smem = kWarps * kRing + 1024;
+  constexpr int smem = kWarps * ring_bytes(D) + 1024;
   CUtensorMap mk, mv;
   if (!page_map<D>(&mk, p.kc, p) || !page_map<D>(&mv, p.vc, p)) return PIQ_ERR_INVALID_ARG;
   static std::atomic<bool> set[2][64];
@@ -745,7 +749,7 @@ int piq_kv8_attention_workspace_bytes(int64_t tokens, int heads, int kv_heads, i
   if (bytes == nullptr ||
       !attn_sizes_ok(tokens, heads, kv_heads, head_dim, batch, max_new, max_len, window))
     return PIQ_ERR_INVALID_ARG;
-  const AttnPlan a = plan_attention(tokens, heads, kv_heads, batch, max_new, max_len, window);
+  const AttnPlan a = plan_attention(tokens, heads, kv_heads, head_dim, batch, max_new, max_len, window);
   *bytes = attn_ws(a, tokens, heads, head_dim).bytes;
   return PIQ_OK;
 }
@@ -770,7 +774,7 @@ int piq_kv8_attention(const void* q, int dtype, int64_t tokens, int64_t ldq, int
   if (q == nullptr || out == nullptr || !ptr_aligned(q, 16) || !ptr_aligned(out, 16) ||
       !ptr_aligned(lse, 4) || workspace == nullptr || !ptr_aligned(workspace, 256))
     return PIQ_ERR_INVALID_ARG;
-  const AttnPlan a = plan_attention(tokens, heads, kv_heads, batch, max_new, max_len, window);
+  const AttnPlan a = plan_attention(tokens, heads, kv_heads, head_dim, batch, max_new, max_len, window);
   const AttnWs w = attn_ws(a, tokens, heads, head_dim);
   if (ws_bytes < w.bytes) return PIQ_ERR_WORKSPACE_TOO_SMALL;
   int rc = injected_fault();
