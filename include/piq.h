@@ -384,7 +384,9 @@ int piq_upper_factor_noalloc(const float* H, int64_t in, float damp, const int32
  * Conventions of these entries, besides the ones above: `dtype` is the type of
  * the unquantized tensors; row strides (ld*) are in elements; the calls only
  * enqueue and never synchronize, so they can be captured into a graph, and no
- * two of them share state except the buffers they are given.  `status` is a
+ * two of them share state except the buffers they are given: calls that may
+ * run at the same time (other streams, graphs replayed side by side) need a
+ * workspace each, and no output may overlap an input.  `status` is a
  * device int32[2] or NULL: what the device finds wrong (a page number or a
  * length out of range, a wait that gave up) is recorded there as {PIQ_ERR_*, detail}, the
  * first one staying until the caller clears it; either way no access leaves
@@ -412,8 +414,8 @@ int piq_int8_quantize_rows(const void* X, int dtype, int64_t rows, int64_t cols,
  *   Y        device [tokens, out] of X's dtype, row stride ldy >= out.
  * tokens >= 0; in % 8 == 0, 8 <= in <= 131064 (the int32 sums stay exact for
  * every code, -128 among them); 1 <= out <= 2^24.
- * Workspace: piq_int8_linear_workspace_bytes (0 for a few tokens: then it may be
- * NULL). */
+ * Workspace: piq_int8_linear_workspace_bytes (0 for one token of up to 16384
+ * values: then it may be NULL). */
 int piq_int8_linear_workspace_bytes(int64_t tokens, int64_t out, int64_t in, size_t* bytes);
 int piq_int8_linear(const void* X, int dtype, int64_t tokens, int64_t in, int64_t ldx,
                     const int8_t* W, int64_t out, int64_t ldw, const float* w_scale,
@@ -474,6 +476,7 @@ int piq_kv8_read(const int8_t* k_codes, const int8_t* v_codes, const float* k_sc
  *           batch: they size the launch and the workspace (a sequence above
  *           them is an error: its rows are NaN).
  *           max_len <= 2^26.
+ *   scale   |scale| <= 2^127.
  *   heads   a multiple of kv_heads, at most 256 kv_heads; tokens <= 2^24 and
  *           tokens * heads < 2^31 - 256.
  * Queries of bf16 are scaled by a power of two a row and used in fp16, exact for

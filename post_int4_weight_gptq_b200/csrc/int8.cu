@@ -130,27 +130,28 @@ int launch_quantize_rows(const void* X, int dtype, int64_t rows, int64_t cols, i
   }
 }
 
-// ------------------------------------------------------- a few tokens, one kernel
+// ----------------------------------------------------------- one token, one kernel
 // A warp takes one output channel: its weights stream through registers in 16-byte
 // pieces (4 KB a warp under way), asked for before anything else, so that the wait
-// for them covers the quantization of the tokens, which every CTA does for itself
-// into shared memory (a token is 2 in bytes from L2).  One launch, no workspace.
-// Bound by the weights' bytes where they are many, by the launch and one trip to
-// memory where they are few: one token, 4096 -> 4096, took 7.3 us as two kernels.
-constexpr int kFewWarps = 8;
+// for them covers the quantization of the token, which every CTA does for itself into
+// shared memory (2 in bytes from L2).  One launch, no workspace.  Bound by the launch
+// and one trip to memory: 4.5 us for 4096 -> 4096 (3.7 TB/s), 7.0 us as two kernels.
+// More tokens gain nothing by it (two kernels second, in us): 2 tokens 7.3 and 6.8-7.0,
+// 4 tokens 10.5 and 7.0, 4 from 4096 to 11008 23.0 and 13.3: all CTAs quantize all
+// tokens, and a weight piece meets as many pieces of codes in shared memory.
+constexpr int kOneWarps = 8;
 constexpr int kPieces = 8;  // 16-byte weight pieces a lane has under way
 
-template <typename T, int TOK>
-__global__ void __launch_bounds__(32 * kFewWarps)
-    int8_few_kernel(const T* __restrict__ X, int tokens, int in, int64_t ldx,
-                    const int8_t* __restrict__ W, int64_t out, int64_t ldw,
-                    const float* __restrict__ sw, const float* __restrict__ bias,
-                    T* __restrict__ Y, int64_t ldy) {
-  extern __shared__ __align__(16) int8_t codes[];  // [TOK][row], zeros behind `in`
-  __shared__ uint32_t red[TOK][kFewWarps];
+template <typename T>
+__global__ void __launch_bounds__(32 * kOneWarps)
+    int8_one_kernel(const T* __restrict__ X, int in, const int8_t* __restrict__ W, int64_t out,
+                    int64_t ldw, const float* __restrict__ sw, const float* __restrict__ bias,
+                    T* __restrict__ Y) {
+  extern __shared__ __align__(16) int8_t codes[];  // `in` padded to 16 with zeros
+  __shared__ uint32_t red[kOneWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = (in + 15) & ~15;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * kFewWarps + warp;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * kOneWarps + warp;
   pdl_launch_dependents();
   pdl_wait();
   const int8_t* w = W + (c < out ? c : 0) * ldw;
@@ -170,86 +171,60 @@ __global__ void __launch_bounds__(32 * kFewWarps)
   const float sc = c < out ? __ldg(sw + c) : 0.0f;
   const float bc = bias != nullptr && c < out ? __ldg(bias + c) : 0.0f;
 
-  Largest<T> top[TOK];
-  for (int k = 8 * threadIdx.x; k < in; k += 8 * 32 * kFewWarps)
-#pragma unroll
-    for (int t = 0; t < TOK; ++t) {
-      Eight<T> e;
-      e.load(X + min(t, tokens - 1) * ldx + k);
-      top[t].add(e);
-    }
-#pragma unroll
-  for (int t = 0; t < TOK; ++t) {
-    const uint32_t m = __reduce_max_sync(0xffffffffu, top[t].bits());
-    if (lane == 0) red[t][warp] = m;
+  Largest<T> top;
+  for (int k = 8 * threadIdx.x; k < in; k += 8 * 32 * kOneWarps) {
+    Eight<T> e;
+    e.load(X + k);
+    top.add(e);
   }
+  const uint32_t m = __reduce_max_sync(0xffffffffu, top.bits());
+  if (lane == 0) red[warp] = m;
   __syncthreads();
-  float scale[TOK], inv[TOK];
-#pragma unroll
-  for (int t = 0; t < TOK; ++t) {
-    scale[t] = scale_of(__reduce_max_sync(0xffffffffu, red[t][lane % kFewWarps]));
-    inv[t] = inverse_of(scale[t]);
-  }
-  for (int k = 8 * threadIdx.x; k < row; k += 8 * 32 * kFewWarps)
-#pragma unroll
-    for (int t = 0; t < TOK; ++t) {
-      uint2 q = make_uint2(0u, 0u);
-      if (k < in) {
-        Eight<T> e;
-        float f[8];
-        e.load(X + min(t, tokens - 1) * ldx + k);
-        e.floats(f);
-        q = codes8(f, inv[t]);
-      }
-      *reinterpret_cast<uint2*>(codes + t * row + k) = q;
+  const float scale = scale_of(__reduce_max_sync(0xffffffffu, red[lane % kOneWarps]));
+  const float inv = inverse_of(scale);
+  for (int k = 8 * threadIdx.x; k < row; k += 8 * 32 * kOneWarps) {
+    uint2 q = make_uint2(0u, 0u);
+    if (k < in) {
+      Eight<T> e;
+      float f[8];
+      e.load(X + k);
+      e.floats(f);
+      q = codes8(f, inv);
     }
+    *reinterpret_cast<uint2*>(codes + k) = q;
+  }
   __syncthreads();
 
-  int acc[TOK] = {};
+  int acc = 0;
   for (int k0 = 0; k0 < in; k0 += 512 * kPieces) {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int k = k0 + 16 * lane + 512 * i;
       if (k >= in) break;
-#pragma unroll
-      for (int t = 0; t < TOK; ++t) {
-        const uint4 b = *reinterpret_cast<const uint4*>(codes + t * row + k);
-        acc[t] = __dp4a(static_cast<int>(a[i].x), static_cast<int>(b.x), acc[t]);
-        acc[t] = __dp4a(static_cast<int>(a[i].y), static_cast<int>(b.y), acc[t]);
-        acc[t] = __dp4a(static_cast<int>(a[i].z), static_cast<int>(b.z), acc[t]);
-        acc[t] = __dp4a(static_cast<int>(a[i].w), static_cast<int>(b.w), acc[t]);
-      }
+      const uint4 b = *reinterpret_cast<const uint4*>(codes + k);
+      acc = __dp4a(static_cast<int>(a[i].x), static_cast<int>(b.x), acc);
+      acc = __dp4a(static_cast<int>(a[i].y), static_cast<int>(b.y), acc);
+      acc = __dp4a(static_cast<int>(a[i].z), static_cast<int>(b.z), acc);
+      acc = __dp4a(static_cast<int>(a[i].w), static_cast<int>(b.w), acc);
       a[i] = load(k + 512 * kPieces);
     }
   }
-#pragma unroll
-  for (int t = 0; t < TOK; ++t) {
-    acc[t] = __reduce_add_sync(0xffffffffu, acc[t]);
-    if (lane == t && t < tokens && c < out)
-      Y[t * ldy + c] = from_float<T>(fmaf(static_cast<float>(acc[t]) * scale[t], sc, bc));
-  }
+  acc = __reduce_add_sync(0xffffffffu, acc);
+  if (lane == 0 && c < out) Y[c] = from_float<T>(fmaf(static_cast<float>(acc) * scale, sc, bc));
 }
 
-// Tokens that the kernel above takes: its CTAs all quantize them, which stops
-// paying when that reads as much as a CTA's weights.
-constexpr int64_t kFewTokens = 1, kFewValues = 16384;
-bool few_tokens(int64_t tokens, int64_t in) {
-  return tokens <= kFewTokens && tokens * in <= kFewValues;
-}
+// What the kernel above takes: at 16384 -> 4096 the two ways meet (15.5 and 15.7 us).
+constexpr int64_t kOneValues = 16384;
+bool one_kernel(int64_t tokens, int64_t in) { return tokens == 1 && in <= kOneValues; }
 
 template <typename T>
-int launch_few_t(const T* X, int64_t tokens, int64_t in, int64_t ldx, const int8_t* W, int64_t out,
-                 int64_t ldw, const float* sw, const float* bias, T* Y, int64_t ldy,
-                 cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(ceil_div(out, kFewWarps));
-  const int tok = tokens == 1 ? 1 : tokens == 2 ? 2 : 4;
-  const size_t smem = static_cast<size_t>(tok) * ((in + 15) / 16 * 16);  // at most 32 KB
-  auto kern = tok == 1 ? int8_few_kernel<T, 1> : tok == 2 ? int8_few_kernel<T, 2>
-                                                          : int8_few_kernel<T, 4>;
+int launch_one_t(const T* X, int64_t in, const int8_t* W, int64_t out, int64_t ldw,
+                 const float* sw, const float* bias, T* Y, cudaStream_t stream) {
+  const unsigned grid = static_cast<unsigned>(ceil_div(out, kOneWarps));
+  const size_t smem = static_cast<size_t>((in + 15) / 16 * 16);
   note_launch();
-  return launch_pdl(kern, dim3(grid), dim3(32 * kFewWarps), smem, stream, X,
-                    static_cast<int>(tokens), static_cast<int>(in), ldx, W, out, ldw, sw, bias, Y,
-                    ldy) == cudaSuccess
+  return launch_pdl(int8_one_kernel<T>, dim3(grid), dim3(32 * kOneWarps), smem, stream, X,
+                    static_cast<int>(in), W, out, ldw, sw, bias, Y) == cudaSuccess
              ? PIQ_OK
              : PIQ_ERR_CUDA;
 }
@@ -261,7 +236,7 @@ struct LinearWs {
 };
 LinearWs linear_ws(int64_t tokens, int64_t in) {
   LinearWs w;
-  if (few_tokens(tokens, in)) return LinearWs{0, 0, 0};
+  if (one_kernel(tokens, in)) return LinearWs{0, 0, 0};
   w.ldq = (in + 15) / 16 * 16;
   w.scale_at = (static_cast<size_t>(std::max<int64_t>(tokens, 1)) * w.ldq + 255) / 256 * 256;
   w.bytes = w.scale_at + (static_cast<size_t>(std::max<int64_t>(tokens, 1)) * 4 + 255) / 256 * 256;
@@ -314,7 +289,7 @@ int piq_int8_linear(const void* X, int dtype, int64_t tokens, int64_t in, int64_
   if (X == nullptr || W == nullptr || w_scale == nullptr || Y == nullptr || !ptr_aligned(X, 16) ||
       !ptr_aligned(W, 16) || !ptr_aligned(w_scale, 4) || !ptr_aligned(bias, 4) ||
       !ptr_aligned(Y, dtype == PIQ_FP32 ? 4 : 2) || !ptr_aligned(status, 4) ||
-      (workspace == nullptr && !few_tokens(tokens, in)) || !ptr_aligned(workspace, 256))
+      (workspace == nullptr && !one_kernel(tokens, in)) || !ptr_aligned(workspace, 256))
     return PIQ_ERR_INVALID_ARG;
   const LinearWs w = linear_ws(tokens, in);
   if (ws_bytes < w.bytes) return PIQ_ERR_WORKSPACE_TOO_SMALL;
@@ -323,17 +298,17 @@ int piq_int8_linear(const void* X, int dtype, int64_t tokens, int64_t in, int64_
   if (rc == PIQ_OK) rc = device_info(&info);
   if (rc != PIQ_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (few_tokens(tokens, in)) {
+  if (one_kernel(tokens, in)) {
     switch (dtype) {
       case PIQ_BF16:
-        return launch_few_t(static_cast<const __nv_bfloat16*>(X), tokens, in, ldx, W, out, ldw,
-                            w_scale, bias, static_cast<__nv_bfloat16*>(Y), ldy, s);
+        return launch_one_t(static_cast<const __nv_bfloat16*>(X), in, W, out, ldw, w_scale, bias,
+                            static_cast<__nv_bfloat16*>(Y), s);
       case PIQ_FP16:
-        return launch_few_t(static_cast<const __half*>(X), tokens, in, ldx, W, out, ldw, w_scale,
-                            bias, static_cast<__half*>(Y), ldy, s);
+        return launch_one_t(static_cast<const __half*>(X), in, W, out, ldw, w_scale, bias,
+                            static_cast<__half*>(Y), s);
       default:
-        return launch_few_t(static_cast<const float*>(X), tokens, in, ldx, W, out, ldw, w_scale,
-                            bias, static_cast<float*>(Y), ldy, s);
+        return launch_one_t(static_cast<const float*>(X), in, W, out, ldw, w_scale, bias,
+                            static_cast<float*>(Y), s);
     }
   }
   int8_t* qx = static_cast<int8_t*>(workspace);

@@ -120,9 +120,12 @@ __device__ __forceinline__ void store_tokens(const GemmArgs& p, T* stage, const 
   for (int i = 0; i < N / 4; ++i) {
     const float4 s = sx4[i];
     stage[(4 * i) * 32 + lane] = from_float<T>(scaled(__float_as_int(f[4 * i]), s.x, sw, bias));
-    stage[(4 * i + 1) * 32 + lane] = from_float<T>(scaled(__float_as_int(f[4 * i + 1]), s.y, sw, bias));
-    stage[(4 * i + 2) * 32 + lane] = from_float<T>(scaled(__float_as_int(f[4 * i + 2]), s.z, sw, bias));
-    stage[(4 * i + 3) * 32 + lane] = from_float<T>(scaled(__float_as_int(f[4 * i + 3]), s.w, sw, bias));
+    stage[(4 * i + 1) * 32 + lane] =
+        from_float<T>(scaled(__float_as_int(f[4 * i + 1]), s.y, sw, bias));
+    stage[(4 * i + 2) * 32 + lane] =
+        from_float<T>(scaled(__float_as_int(f[4 * i + 2]), s.z, sw, bias));
+    stage[(4 * i + 3) * 32 + lane] =
+        from_float<T>(scaled(__float_as_int(f[4 * i + 3]), s.w, sw, bias));
   }
   __syncwarp();
 #pragma unroll
@@ -466,13 +469,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpi, 1)
         float4 sx[8];
         if (t0 + i0 + 32 <= p.tokens) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sx[i] = __ldg(reinterpret_cast<const float4*>(p.sx + t0 + i0) + i);
+          for (int i = 0; i < 8; ++i)
+            sx[i] = __ldg(reinterpret_cast<const float4*>(p.sx + t0 + i0) + i);
         } else {
           const int last = p.tokens - 1, at = t0 + i0;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            sx[i] = make_float4(__ldg(p.sx + min(at + 4 * i, last)), __ldg(p.sx + min(at + 4 * i + 1, last)),
-                                __ldg(p.sx + min(at + 4 * i + 2, last)), __ldg(p.sx + min(at + 4 * i + 3, last)));
+            sx[i] = make_float4(__ldg(p.sx + min(at + 4 * i, last)),
+                                __ldg(p.sx + min(at + 4 * i + 1, last)),
+                                __ldg(p.sx + min(at + 4 * i + 2, last)),
+                                __ldg(p.sx + min(at + 4 * i + 3, last)));
         }
         store_tokens<T, 32>(p, stage, f, sx, t0 + i0, c - lane, sw, bias, lane);
       }
@@ -561,7 +567,7 @@ int gemm_t(const int8_t* qx, int64_t ldq, const int8_t* W, int64_t ldw, GemmArgs
   if (a.pair) {
     p.m_tiles = static_cast<int>(ceil_div(p.out, 2 * BM));
     const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
-    if (tiles > INT32_MAX) return PIQ_ERR_INVALID_ARG;
+    if (tiles > INT32_MAX - sms) return PIQ_ERR_INVALID_ARG;
     const int pairs = static_cast<int>(std::min<int64_t>(tiles, sms / 2));
     const int i = a.nt == 256;
     return launch_gemm(pair[i], slot0 + i, dim3(2 * pairs), 64 + 32 * kEpi,
@@ -571,8 +577,8 @@ int gemm_t(const int8_t* qx, int64_t ldq, const int8_t* W, int64_t ldw, GemmArgs
   p.slices = a.slices;
   int i = 0;
   while (16 << i < a.nt) ++i;
-  return launch_gemm(split[i], slot0 + 2 + i, dim3(a.slices * p.m_tiles, p.n_tiles), 192, split_ring(a.nt), a.slices,
-                     stream, mw, mx, p);
+  return launch_gemm(split[i], slot0 + 2 + i, dim3(a.slices * p.m_tiles, p.n_tiles), 192,
+                     split_ring(a.nt), a.slices, stream, mw, mx, p);
 }
 
 }  // namespace

@@ -257,7 +257,8 @@ bool kv8_cache_ok(const void* kc, const void* vc, const void* ks, const void* vs
                   int heads, int head_dim, int block) {
   return kc != nullptr && vc != nullptr && ks != nullptr && vs != nullptr && ptr_aligned(kc, 16) &&
          ptr_aligned(vc, 16) && ptr_aligned(ks, 4) && ptr_aligned(vs, 4) && pages >= 1 &&
-         pages <= INT32_MAX && heads >= 1 && heads <= 1024 && pages * heads <= INT32_MAX && (head_dim == 64 || head_dim == 128) &&
+         pages <= INT32_MAX && heads >= 1 && heads <= 1024 && pages * heads <= INT32_MAX &&
+         (head_dim == 64 || head_dim == 128) &&
          (block == 16 || block == 32 || block == 64 || block == 128);
 }
 

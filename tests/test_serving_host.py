@@ -59,10 +59,10 @@ def test_linear_workspace(lib):
     assert linear(lib, tokens=0, X=None, Y=None, work=None) == piq.PIQ_OK
     a, b = piq.int8_linear_workspace_bytes(40, 32, 64), piq.int8_linear_workspace_bytes(400, 32, 64)
     assert 0 < a <= b
-    # a few tokens run as one kernel without a workspace; long rows or more tokens do not
-    assert piq.int8_linear_workspace_bytes(4, 32, 4096) == 0
-    assert piq.int8_linear_workspace_bytes(4, 32, 4104) > 0
-    assert piq.int8_linear_workspace_bytes(5, 32, 64) > 0
+    # one token runs as one kernel without a workspace; a long one, or more, do not
+    assert piq.int8_linear_workspace_bytes(1, 32, 16384) == 0
+    assert piq.int8_linear_workspace_bytes(1, 32, 16392) > 0
+    assert piq.int8_linear_workspace_bytes(2, 32, 64) > 0
     out = ctypes.c_size_t()
     assert lib.piq_int8_linear_workspace_bytes(4, 32, 60, ctypes.byref(out)) < 0
     assert lib.piq_int8_linear_workspace_bytes(4, 32, 64, None) < 0
