@@ -33,6 +33,7 @@
 // is lost.  The sum of p stays in fp32.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "kv8_attn.cuh"
@@ -281,13 +282,15 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
       const int row = row0 + 8 * t + 2 * c + e;
       rs[t][e] = s_rs[8 * t + 2 * c + e];
       qs[t][e] = s_qs[8 * t + 2 * c + e];
-      hi[t][e] = row < rows ? len - n + static_cast<int>(static_cast<unsigned>(row) / p.group) + 1 - k0 : 0;
+      const int tok = static_cast<int>(static_cast<unsigned>(row) / p.group);
+      hi[t][e] = row < rows ? len - n + tok + 1 - k0 : 0;
     }
   }
   // tiles in which every row sees every key need no masks
   const unsigned last_tok = static_cast<unsigned>(min(row0 + ROWS, rows) - 1) / p.group;
   const unsigned first_tok = static_cast<unsigned>(row0) / p.group;
-  const int all_lo = window > 0 ? max(len - n + static_cast<int>(last_tok) + 1 - window - k0, 0) : 0;
+  const int all_lo =
+      window > 0 ? max(len - n + static_cast<int>(last_tok) + 1 - window - k0, 0) : 0;
   const int all_hi = row0 + ROWS <= rows ? len - n + static_cast<int>(first_tok) + 1 - k0 : 0;
 
   float m[NT][2], l[NT][2], o[NT][KS][4];
@@ -458,7 +461,8 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
     else
       process(step, std::false_type());
     __syncwarp();  // every lane has read the stage
-    if (lane == 0 && step + STAGES * kWarps < steps) fetch(step + STAGES * kWarps, stage, [&](int i) { return s_page[i]; });
+    if (lane == 0 && step + STAGES * kWarps < steps)
+      fetch(step + STAGES * kWarps, stage, [&](int i) { return s_page[i]; });
     if (++stage == STAGES) {
       stage = 0;
       phase ^= 1u;
@@ -618,7 +622,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv8_join_kernel(Kv8Attn p) {
 // more than it spreads; where they do, chunks that even out ragged lengths.
 constexpr int64_t kMinChunk = 256, kManyCtasChunk = 2048, kMaxChunk = 4096;
 constexpr int64_t kMinPromptChunk = 512;
-constexpr int64_t kManyRows = 16;  // rows a kv head above which the tensor-memory kernel runs
+// Rows a kv head above which the tensor-memory kernel runs.  Groups of 16 rows here each
+// read the codes again, mostly from L2; there the time hardly depends on the rows.
+// Here and there in us, 8 sequences of 4096 keys and 8 kv heads: dim 128, 16 rows 29.5
+// and 58.7, 32 rows 53.1 and 66.5, 48 rows 76 and 70; dim 64, 32 rows 29 and 55, 48 rows
+// 46 and 58.  48 such sequences: dim 128, 32 rows 281 and 289, 48 rows 406 and 289;
+// dim 64, 48 rows 208 and 250.
+constexpr int64_t many_rows(int dim) { return dim == 64 ? 48 : 32; }
 
 struct AttnPlan {
   bool prompt;       // kv8_prompt.cu
@@ -628,14 +638,15 @@ struct AttnPlan {
   int chunks;
 };
 
-AttnPlan plan_attention(int64_t tokens, int heads, int kv_heads, int head_dim, int64_t batch, int64_t max_new, int64_t max_len,
-                        int64_t window) {
+AttnPlan plan_attention(int64_t tokens, int heads, int kv_heads, int head_dim, int64_t batch,
+                        int64_t max_new, int64_t max_len, int64_t window) {
   AttnPlan a;
   a.window = window < max_len ? static_cast<int>(window) : 0;  // a wider one hides nothing
-  const int64_t rows = std::min(max_new, tokens) * (heads / kv_heads);
-  a.prompt = rows > kManyRows;
+  const int64_t rows = std::min(std::max<int64_t>(max_new, 1), std::max<int64_t>(tokens, 1)) *
+                       (heads / kv_heads);
+  a.prompt = rows > many_rows(head_dim);
   a.nt = rows <= 8 ? 1 : 2;
-  a.row_groups = std::max<int64_t>(1, ceil_div(rows, 8 * a.nt));
+  a.row_groups = ceil_div(rows, 8 * a.nt);
   int64_t span = max_len;  // most keys in sight of a sequence, from a block's (at most 128) start
   if (a.window > 0) span = std::min(span, window + max_new + 128);
   span = std::max<int64_t>(span, 1);
@@ -710,7 +721,8 @@ int launch_attention(const Kv8Attn& p, const AttnPlan& a, cudaStream_t stream) {
     if (rc != PIQ_OK) return rc;
     return a.chunks == 1 ? PIQ_OK : launch_join<T, D>(p, stream);
   }
-  void (*kern)(CUtensorMap, CUtensorMap, Kv8Attn) = a.nt == 1 ? kv8_chunk_kernel<T, D, 1> : kv8_chunk_kernel<T, D, 2>;
+  void (*kern)(CUtensorMap, CUtensorMap, Kv8Attn) =
+      a.nt == 1 ? kv8_chunk_kernel<T, D, 1> : kv8_chunk_kernel<T, D, 2>;
   const unsigned gx = static_cast<unsigned>(a.row_groups * p.kv_heads);
   constexpr int smem = kWarps * ring_bytes(D) + 1024;
   CUtensorMap mk, mv;
@@ -720,7 +732,8 @@ int launch_attention(const Kv8Attn& p, const AttnPlan& a, cudaStream_t stream) {
   if (cudaGetDevice(&dev) != cudaSuccess) return PIQ_ERR_CUDA;
   std::atomic<bool>* done = dev < 64 ? &set[a.nt - 1][dev] : nullptr;
   if (done == nullptr || !done->load(std::memory_order_acquire)) {
-    const int rc = cuda_rc(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    const int rc =
+        cuda_rc(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     if (rc != PIQ_OK) return rc;
     if (done != nullptr) done->store(true, std::memory_order_release);
   }
@@ -749,7 +762,8 @@ int piq_kv8_attention_workspace_bytes(int64_t tokens, int heads, int kv_heads, i
   if (bytes == nullptr ||
       !attn_sizes_ok(tokens, heads, kv_heads, head_dim, batch, max_new, max_len, window))
     return PIQ_ERR_INVALID_ARG;
-  const AttnPlan a = plan_attention(tokens, heads, kv_heads, head_dim, batch, max_new, max_len, window);
+  const AttnPlan a =
+      plan_attention(tokens, heads, kv_heads, head_dim, batch, max_new, max_len, window);
   *bytes = attn_ws(a, tokens, heads, head_dim).bytes;
   return PIQ_OK;
 }
@@ -766,15 +780,16 @@ int piq_kv8_attention(const void* q, int dtype, int64_t tokens, int64_t ldq, int
       !attn_sizes_ok(tokens, heads, kv_heads, head_dim, batch, max_new, max_len, window) ||
       !kv8_cache_ok(k_codes, v_codes, k_scale, v_scale, pages, kv_heads, head_dim, block) ||
       !kv8_table_ok(cu_q, lens, batch, block_table, table_width, ldt, status) ||
-      !(scale == scale) || scale - scale != 0.0f)
+      !(std::fabs(scale) <= 0x1p127f))  // scale log2(e) is finite
     return PIQ_ERR_INVALID_ARG;
   const int64_t row = static_cast<int64_t>(heads) * head_dim;
   if (ldq < row || ldo < row || ldq % 8 != 0 || ldo % 8 != 0) return PIQ_ERR_INVALID_ARG;
-  if (tokens == 0 || max_new == 0) return PIQ_OK;
+  if (tokens == 0) return PIQ_OK;
   if (q == nullptr || out == nullptr || !ptr_aligned(q, 16) || !ptr_aligned(out, 16) ||
       !ptr_aligned(lse, 4) || workspace == nullptr || !ptr_aligned(workspace, 256))
     return PIQ_ERR_INVALID_ARG;
-  const AttnPlan a = plan_attention(tokens, heads, kv_heads, head_dim, batch, max_new, max_len, window);
+  const AttnPlan a =
+      plan_attention(tokens, heads, kv_heads, head_dim, batch, max_new, max_len, window);
   const AttnWs w = attn_ws(a, tokens, heads, head_dim);
   if (ws_bytes < w.bytes) return PIQ_ERR_WORKSPACE_TOO_SMALL;
   int rc = injected_fault();

@@ -335,7 +335,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
   Shared& sh = *reinterpret_cast<Shared*>(smem + L::BAR_AT);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  pdl_launch_dependents();
   pdl_wait();
   // ------------------------------------------------------------- which rows
   // Items of 256 rows are numbered without the lengths: sequence b's start at
@@ -412,6 +411,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  // behind the allocation: a kernel that starts early must not hold tensor memory that
+  // this one still waits for
+  pdl_launch_dependents();
   // the largest value scale, found by the widening warps
   auto find_vmax = [&]() {
     const int b0 = k0 >> shift, b1 = (k1 - 1) >> shift;

@@ -602,3 +602,135 @@ def test_binding_refuses_what_does_not_fit():
     with pytest.raises(piq.PiqError):
         piq.kv8_attention(c, torch.zeros(1, 3, 64, dtype=BF16, device="cuda"), cu, lens, table,
                           1, 1)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("group,new", [(17, 1), (8, 3), (8, 4), (11, 3), (8, 5), (16, 3), (7, 7),
+                                       (32, 2)])
+def test_attention_where_the_kernels_meet(dtype, dim, group, new):
+    # rows a kv head from 17 to 64: groups of rows on one side, one tile of them on the other
+    rng = np.random.default_rng(100 * group + new)
+    b = Batch(rng, [700, 90, 330], 2, dim, 32, dtype)
+    b.append([650, 10, 300])
+    news = [new, 1, max(new - 1, 1)]
+    b.append(news)
+    q = rand(rng, (sum(news), 2 * group, dim), dtype)
+    for window, max_len in ((0, max(b.lens)), (100, max(b.lens)), (0, 40000)):
+        out, lse = run_attention(b, q, news, max_len, window)
+        check_attention(b, q, news, out, lse, window)
+
+
+@pytest.mark.parametrize("heads,news", [(4, [1, 2, 1]), (8, [30, 64, 20])])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attention_bad_page_reaches_its_readers_only(dim, heads, news):
+    # a bad page in the middle of one sequence's new tokens: queries before it see nothing of it
+    rng = np.random.default_rng(21)
+    b = Batch(rng, [200, 200, 200], 2, dim, 16, BF16)
+    b.append([100, 127, 90])
+    b.append(news)
+    q = rand(rng, (sum(news), heads, dim), BF16)
+    good, _ = run_attention(b, q, news)
+    table = b.gpu_table().clone()
+    table[1, 128 // 16] = -7                       # positions 128 ..; the new ones start at 127
+    status = piq.new_status()
+    cu = [0, *np.cumsum(news).tolist()]
+    out = piq.kv8_attention(b.cache, q, ints(cu), ints(b.lens), table, max(news), max(b.lens),
+                            status=status)
+    assert status.tolist() == [piq.PIQ_ERR_INVALID_ARG, 1]
+    first = cu[1] + 1
+    assert torch.isnan(out[first:cu[2]]).all()
+    keep = [i for i in range(sum(news)) if not first <= i < cu[2]]
+    assert torch.isfinite(out[keep]).all()
+    # the value scales of the page are gone too, so the scaling of probabilities may move:
+    # their roundings, 2^-11 on either side, of values below 8, and one of the result each
+    assert worst(np.abs(f64(out[keep]) - f64(good[keep])),
+                 np.abs(f64(good[keep])) * 2.02 * half_step(BF16) + 2.0 ** -7) <= 1
+
+
+def test_rows_of_no_sequence_and_no_new_tokens():
+    rng = np.random.default_rng(22)
+    b = Batch(rng, [40, 40], 2, 64, 16, BF16)
+    b.append([20, 30])
+    q = rand(rng, (5, 4, 64), BF16)
+    out = torch.full_like(q, 7.0)
+    status = piq.new_status()
+    piq.kv8_attention(b.cache, q, ints([0, 0, 0]), ints(b.lens), b.gpu_table(), 0, 40, out=out,
+                      status=status)
+    assert (out == 7).all() and status.tolist() == [0, 0]
+    # max_new below what the lengths say is an error, not silence
+    piq.kv8_attention(b.cache, q, ints([0, 1, 1]), ints(b.lens), b.gpu_table(), 0, 40, out=out,
+                      status=status)
+    assert torch.isnan(out[0]).all() and (out[1:] == 7).all()
+    assert status.tolist() == [piq.PIQ_ERR_INVALID_ARG, 0]
+    with pytest.raises(piq.PiqError):
+        piq.kv8_attention(b.cache, q, ints([0, 1, 1]), ints(b.lens), b.gpu_table(), 1, 40,
+                          scale=3e38)
+
+
+def test_captured_calls_of_every_kernel():
+    # prompts back to back, split and joined keys and every form of the product, captured
+    # twice with workspaces of their own and replayed side by side on new inputs
+    rng = np.random.default_rng(23)
+    b = Batch(rng, [1200, 3000], 2, 128, 64, BF16)
+    b.append([900, 2800])
+    b.append([100, 90])
+    q = torch.zeros(190, 8, 128, dtype=BF16, device="cuda")
+    step = torch.zeros(2, 8, 128, dtype=BF16, device="cuda")
+    lin = [linear_case(rng, t, 1032, 520, BF16, True) for t in (1, 30, 200, 1500)]
+    cu, one, lens, table = ints([0, 100, 190]), ints([0, 1, 2]), ints(b.lens), b.gpu_table()
+
+    def work():
+        got = [piq.kv8_attention(b.cache, q, cu, lens, table, 100, 3000) for _ in range(2)]
+        got.append(piq.kv8_attention(b.cache, step, one, lens, table, 1, 100000))
+        return got + [piq.int8_linear(*c) for c in lin]
+
+    work()
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(work())
+        graphs.append(g)
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        q.copy_(rand(rng, q.shape, BF16))
+        step.copy_(rand(rng, step.shape, BF16))
+        for c in lin:
+            c[0].copy_(rand(rng, c[0].shape, BF16))
+        want = work()
+        torch.cuda.synchronize()
+        graphs[0].replay()
+        with torch.cuda.stream(side):
+            graphs[1].replay()
+        torch.cuda.synchronize()
+        for got in outs:
+            for x, y in zip(got, want):
+                assert torch.equal(x, y)
+
+
+def test_default_stream_given_by_handle():
+    rng = np.random.default_rng(24)
+    x, w, ws, bias = linear_case(rng, 9, 520, 264, FP16, True)
+    want = piq.int8_linear(x, w, ws, bias)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):                  # another stream is current
+        got = piq.int8_linear(x, w, ws, bias, stream=torch.cuda.default_stream())
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_quantized_weights_used_at_once():
+    # the product asks for the weights before the kernels ahead of it end, but not before
+    # the one that writes them has ended
+    rng = np.random.default_rng(25)
+    x = rand(rng, (40, 4096), BF16)
+    for i in range(10):
+        w = rand(rng, (1024, 4096), BF16)
+        torch.cuda.synchronize()
+        codes, scale = piq.int8_quantize_rows(w)
+        y = piq.int8_linear(x, codes, scale)
+        torch.cuda.synchronize()
+        assert torch.equal(y, piq.int8_linear(x, codes, scale))
