@@ -586,8 +586,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
       const int t = warp >> 2;
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t ts = tmem + lanes + t * KT, to = tmem + lanes + 2 * KT + t * D;
-      const int hi = live ? len - n + static_cast<int>(rel) + 1 : 0;
-      const int lo = p.window > 0 ? hi - p.window : 0;
+      // Keys [lo, hi) are this row's, of those before the part's end: with a window the
+      // tiles start where it does, and the last one may reach into the next part.
+      const int end = len - n + static_cast<int>(rel) + 1;
+      const int hi = live ? min(end, c1) : 0;
+      const int lo = p.window > 0 ? end - p.window : 0;
       float m = kLow;
       uint64_t l2 = 0;  // the sum, even and odd keys
       bool ok = true;

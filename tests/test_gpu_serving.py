@@ -734,3 +734,19 @@ def test_quantized_weights_used_at_once():
         y = piq.int8_linear(x, codes, scale)
         torch.cuda.synchronize()
         assert torch.equal(y, piq.int8_linear(x, codes, scale))
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim,block,news,lens,window", [
+    (1, 1, 64, 128, [226, 132], [1224, 221], 240), (2, 2, 128, 128, [226, 100], [1224, 1000], 240),
+    (4, 1, 64, 32, [100, 64, 30], [1500, 900, 1111], 333), (8, 2, 128, 16, [70], [2000], 777),
+    (8, 1, 64, 64, [9, 200], [3000, 2500], 1500)])
+def test_attention_window_over_split_keys(heads, kv_heads, dim, block, news, lens, window):
+    # the window's first key is not on the grid of the parts that the keys are split into
+    rng = np.random.default_rng(sum(lens) + window)
+    b = Batch(rng, [n + 50 for n in lens], kv_heads, dim, block, BF16)
+    b.append([total - n for total, n in zip(lens, news)])
+    b.append(news)
+    q = rand(rng, (sum(news), heads, dim), BF16)
+    for w in (window, window + 1, window + 64):
+        out, lse = run_attention(b, q, news, window=w)
+        check_attention(b, q, news, out, lse, w)
