@@ -13,14 +13,10 @@
 // tokens' places in a tile of 16 and the eighths are permuted so that the swizzled
 // reads of eight lanes meet 32 different banks.
 //
-// A byte becomes a half exactly, in two ways.  Values: u = code + 128 under the
-// exponent of 1024 is 1152 + code, minus 1152.  Keys: u in the low bits of a half is
-// the subnormal number u 2^-24, which the tensor cores take as it is, and the 128 is
-// taken off the sum instead, q . k = 2^24 (q . u) - 128 sum(q); that saves the
-// subtraction of every pair and costs two bits of the fp32 sum's 24 (u <= 255
-// against |code| <= 127), nothing beside the rounding of a probability.  For the
-// values it would cost those bits where an output is near 0 beside large values, so
-// they keep the subtraction.
+// A byte becomes a half exactly: u = code + 128 under the exponent of 1024 is 1152 +
+// code, minus 1152.  (Leaving the 128 in and taking it off the sums instead was no
+// faster, 54.6 against 54.4 us for one sequence of 131072 keys, and its cancellation
+// put lse off by 5e-5 where a query has a few loud channels; this way 2e-6.)
 //
 // Keys and values are the wide operand (16 tokens, or 16 dimensions, a
 // product), the queries the narrow one (8 rows), because a decoding step has
@@ -60,13 +56,6 @@ __device__ __forceinline__ void halves_of(uint32_t w, uint32_t low, uint32_t& ev
   even = *reinterpret_cast<const uint32_t*>(&eh);
   odd = *reinterpret_cast<const uint32_t*>(&oh);
 }
-// The same, each + 128 and times 2^-24.
-__device__ __forceinline__ void biased_halves_of(uint32_t w, uint32_t low, uint32_t& even,
-                                                 uint32_t& odd) {
-  even = (w & low) ^ 0x00800080u;
-  odd = ((w >> 8) & low) ^ 0x00800080u;
-}
-
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -119,7 +108,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
   __shared__ int s_page[kMaxPages];  // page kv_heads + head
   __shared__ float s_ks[kMaxPages], s_vs[kMaxPages];
   __shared__ __align__(16) __half s_q[ROWS][D];
-  __shared__ float s_rs[ROWS], s_qs[ROWS];
+  __shared__ float s_rs[ROWS];
   __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS], s_v[kWarps];
   __shared__ uint64_t full[kWarps][STAGES];
   extern __shared__ uint8_t ring_raw[];  // the warps' rings, then the join's buffer
@@ -233,21 +222,13 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
     }
     amax = warp_max(amax);
     if (__any_sync(0xffffffffu, nan)) amax = __uint_as_float(0x7FC00000u);
-    float mul, sum = 0.0f;
+    float mul;
     const float undo = row_exponent<T>(amax, mul);
     const int at = min(warp + i * kWarps, ROWS - 1);
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
-      const __half h = __float2half_rn(undo == undo ? qv[i][j] * mul : 0.0f);
-      s_q[at][32 * j + lane] = h;
-      sum += __half2float(h);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) {
-      s_rs[at] = undo * p.scale2;
-      s_qs[at] = -128.0f * sum;
-    }
+    for (int j = 0; j < D / 32; ++j)
+      s_q[at][32 * j + lane] = __float2half_rn(undo == undo ? qv[i][j] * mul : 0.0f);
+    if (lane == 0) s_rs[at] = undo * p.scale2;
   }
   __syncthreads();
 
@@ -265,7 +246,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
 
   // -------------------------------------------------------------- fragments of q
   uint32_t qf[NT][KS][2];
-  float rs[NT][2], qs[NT][2];
+  float rs[NT][2];
   int hi[NT][2];  // keys of the chunk that rows 2c, 2c + 1 see: j < hi
   const int window = p.window;
 #pragma unroll
@@ -273,7 +254,8 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       // bytes 16 c + 4 w + {0, 2} and {1, 3} of each 64-byte half, w = s % 4
-      const uint2 x = *reinterpret_cast<const uint2*>(&s_q[8 * t + r][64 * (s / 4) + 16 * c + 4 * (s % 4)]);
+      const uint2 x = *reinterpret_cast<const uint2*>(
+          &s_q[8 * t + r][64 * (s / 4) + 16 * c + 4 * (s % 4)]);
       qf[t][s][0] = __byte_perm(x.x, x.y, 0x5410);
       qf[t][s][1] = __byte_perm(x.x, x.y, 0x7632);
     }
@@ -281,7 +263,6 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
     for (int e = 0; e < 2; ++e) {
       const int row = row0 + 8 * t + 2 * c + e;
       rs[t][e] = s_rs[8 * t + 2 * c + e];
-      qs[t][e] = s_qs[8 * t + 2 * c + e];
       const int tok = static_cast<int>(static_cast<unsigned>(row) / p.group);
       hi[t][e] = row < rows ? len - n + tok + 1 - k0 : 0;
     }
@@ -332,8 +313,8 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           uint32_t a0, a1, a2, a3;
-          biased_halves_of(x0[w], low, a0, a2);
-          biased_halves_of(x1[w], low, a1, a3);
+          halves_of(x0[w], low, a0, a2);
+          halves_of(x1[w], low, a1, a3);
 #pragma unroll
           for (int t = 0; t < NT; ++t)
             mma_f16(s[u][t], a0, a1, a2, a3, qf[t][4 * j + w][0], qf[t][4 * j + w][1]);
@@ -348,7 +329,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
         const float f0 = rs[t][0] * kscale[u], f1 = rs[t][1] * kscale[u];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          s[u][t][e] = fmaf(s[u][t][e], 0x1p24f, qs[t][e & 1]) * (e & 1 ? f1 : f0);
+          s[u][t][e] *= e & 1 ? f1 : f0;
           if (MASK) {
             const int j = key0 + 16 * u + tk + 8 * (e >> 1), h = hi[t][e & 1];
             const bool see = j < h && (window == 0 || j >= h - window);

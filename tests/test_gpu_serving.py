@@ -750,3 +750,31 @@ def test_attention_window_over_split_keys(heads, kv_heads, dim, block, news, len
     for w in (window, window + 1, window + 64):
         out, lse = run_attention(b, q, news, window=w)
         check_attention(b, q, news, out, lse, w)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("max_new", [1, 100])
+def test_attention_score_beside_loud_query_channels(dtype, dim, max_new):
+    # One key a query, so lse is its score, a small integer: queries that are loud where the
+    # key is 0 must not take bits from it.  Codes and queries are integers (the largest key is
+    # 127: its scale is 1) and the sum is exact in fp32, so the score is off by the roundings
+    # of scale log2(e) (2), of the two products with it and of ln 2 and the product with that:
+    # at most 6 of 2^-24, and second-order terms.  (max_new picks the kernel.)
+    rng = np.random.default_rng(31)
+    n = 60
+    k, q = np.zeros((n, 1, dim), np.float32), np.zeros((n, 2, dim), np.float32)
+    k[:, 0, :8] = rng.integers(-9, 10, (n, 8))
+    k[:, 0, 0] = 127
+    q[..., :8] = rng.integers(1, 4, (n, 2, 8))
+    q[..., 8:] = 1024 + 8 * rng.integers(0, 64, (n, 2, dim - 8))
+    cache = piq.kv8_cache(n, 1, dim, 16)
+    kt, qt = (torch.from_numpy(a).cuda().to(dtype) for a in (k, q))
+    cu, table = ints(list(range(n + 1))), ints([[i] for i in range(n)])
+    piq.kv8_append(cache, kt, kt, cu, ints([0] * n), table)
+    assert (cache.k_scale == 1).all()
+    out, lse = piq.kv8_attention(cache, qt, cu, ints([1] * n), table, max_new, 1,
+                                 return_lse=True)
+    want = (q.astype(np.float64) * k).sum(2) * dim ** -0.5
+    assert (np.abs(f64(lse) - want) <= 6.1 * 2.0 ** -24 * np.abs(want)).all()
+    assert torch.equal(out, kt.expand(n, 2, dim))
