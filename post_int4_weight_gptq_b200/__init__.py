@@ -15,6 +15,10 @@ Methods (web pages on the subject, cited by title and section):
   alpha per layer by grid search on the calibration output error.
 * AWQ then GPTQ - same page, the serving decision list: the two compose, AWQ's
   scaling first and GPTQ's rounding after (GPTQ on W diag(s), X diag(1/s)).
+
+Beside them, the 8-bit arithmetic of one attention layer: int8_quantize_rows and
+int8_linear, the paged cache kv8_cache with kv8_append and kv8_read, and
+kv8_attention over it.
 """
 from __future__ import annotations
 
