@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
 
   int stage = 0;
   const uint32_t mine_at = smem_u32(mine), low = p.low_bytes;
-  float per_vmax = 0.0f;  // kPScale / vmax
+  float per_vmax = 0.0f;  // 1 / vmax: finite for every scale from 2^-126, kPScale / vmax is not
   uint32_t phase = 0;
   bool ok = true;
   // One step; MASK: some row does not see all of its keys.  Two forms, because the
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
       const float fresh = fmaxf(fmaxf(vscale[0], vscale[1]), vmax);
       const float fv = vmax > 0.0f ? vmax / fresh : 0.0f;
       vmax = fresh;
-      per_vmax = vmax > 0.0f ? kPScale / vmax : 0.0f;
+      per_vmax = vmax > 0.0f ? 1.0f / vmax : 0.0f;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         float f[2];
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
     uint32_t pb[2][NT][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const float vf = vscale[u] * per_vmax;
+      const float vf = vscale[u] * per_vmax * kPScale;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll

@@ -778,3 +778,45 @@ def test_attention_score_beside_loud_query_channels(dtype, dim, max_new):
     want = (q.astype(np.float64) * k).sum(2) * dim ** -0.5
     assert (np.abs(f64(lse) - want) <= 6.1 * 2.0 ** -24 * np.abs(want)).all()
     assert torch.equal(out, kt.expand(n, 2, dim))
+
+
+# ---------------------------------------------------------- values far apart in size
+def put(b, news, k, v):
+    """Appends the given keys and values (fp32 [tokens, heads, dim]) on both sides."""
+    cu = [0, *np.cumsum(news).tolist()]
+    k, v = np.ascontiguousarray(k, np.float32), np.ascontiguousarray(v, np.float32)
+    piq.kv8_append(b.cache, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), ints(cu),
+                   ints(b.lens), b.gpu_table())
+    b.ref.append((k, v), cu, b.lens, b.table)
+    b.lens = [x + n for x, n in zip(b.lens, news)]
+
+
+def check_sizes(b, q, news, out, lse, window=0):
+    """check_attention for bf16 results of any size: the smallest steps are bf16's, 2^-133."""
+    cu = [0, *np.cumsum(news).tolist()]
+    ref, rl, tol, tol_l = S.attention_ref(b.ref, f64(q), cu, b.lens, b.table, q.shape[2] ** -0.5,
+                                          window)
+    assert out.dtype == BF16
+    tol = tol + np.abs(ref) * half_step(BF16) * 1.01 + 2.0 ** -134
+    assert worst(np.abs(f64(out) - ref), tol) <= 1
+    assert worst(np.abs(f64(lse) - rl), tol_l) <= 1
+
+
+@pytest.mark.parametrize("heads,new", [(4, 1), (4, 4)])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("tiny", [400, 320, 32, 1])
+def test_attention_smallest_value_scales(dim, heads, new, tiny):
+    # value scales from the smallest that are kept, 2^-126, in the first blocks or in all
+    rng = np.random.default_rng(dim + tiny)
+    b = Batch(rng, [400], 1, dim, 16, FP32)
+    k, v = rng.normal(0, 1, (2, 400, 1, dim)).astype(np.float32)
+    small = slice(0, -(-tiny // 16) * 16)
+    v[small] *= 3e-37
+    v[small][::16, 0, 5] = 1.6e-36          # each block's largest: above 127 * 2^-126
+    put(b, [400 - new], k[:400 - new], v[:400 - new])
+    put(b, [new], k[400 - new:], v[400 - new:])
+    first = b.ref.scale[1][b.table[0][0]]
+    assert 2.0 ** -126 <= first[0] < 2.0 ** -124
+    q = rand(rng, (new, heads, dim), BF16)
+    for max_len in (400, 40000):
+        check_sizes(b, q, [new], *run_attention(b, q, [new], max_len))
