@@ -480,9 +480,10 @@ int piq_kv8_read(const int8_t* k_codes, const int8_t* v_codes, const float* k_sc
  *   heads   a multiple of kv_heads, at most 256 kv_heads; tokens <= 2^24 and
  *           tokens * heads < 2^31 - 256.
  * Queries of bf16 are scaled by a power of two a row and used in fp16, exact for
- * values down to 2^-14 of the row's largest; probabilities are used in fp16
- * times 2^7, relative to the largest v_scale and probability in sight.  Sums
- * and softmax statistics are fp32.
+ * values down to 2^-14 of the row's largest; probabilities times v_scale are used
+ * in fp16 times 2^7, relative to the largest v_scale and probability that the
+ * query sees (half a step is 2^-11, or 2^-32 of those).  Sums and softmax
+ * statistics are fp32.
  * Workspace: piq_kv8_attention_workspace_bytes with the same sizes. */
 int piq_kv8_attention_workspace_bytes(int64_t tokens, int heads, int kv_heads, int head_dim,
                                       int64_t batch, int64_t max_new, int64_t max_len,

@@ -97,8 +97,8 @@ def attention_ref(cache, q, cu, lens, table, scale, window=0):
     each is off by at most (d + 4) 2^-23 of the sum of magnitudes, B; that is an
     absolute error of a logarithm, to which the exponential adds 2^-20.
     Probabilities are rounded to fp16 (half a step, 2^-11), or, far below the
-    largest, to multiples of 2^-24 / 2^7 of the largest scale (half a step is
-    2^-32 of the largest value, for each key)."""
+    largest, to multiples of 2^-24 / 2^7 of the largest scale that the row sees
+    (half a step is 2^-32 of 127 times it, for each key)."""
     q = np.asarray(q, np.float64)
     rows, heads, d = q.shape
     kvh = cache.codes[0].shape[1]
@@ -110,7 +110,8 @@ def attention_ref(cache, q, cu, lens, table, scale, window=0):
             continue
         k = cache.tokens(0, b, 0, lens[b], table)
         v = cache.tokens(1, b, 0, lens[b], table)
-        vmax = np.abs(v[np.isfinite(v)]).max(initial=0.0)
+        page = np.asarray(table[b])[np.arange(lens[b]) // cache.block]
+        vs = np.asarray(cache.scale[1], np.float64)[page]          # [keys, kv heads]
         for i in range(n):
             p = lens[b] - n + i
             lo = max(0, p + 1 - window) if window else 0
@@ -118,6 +119,8 @@ def attention_ref(cache, q, cu, lens, table, scale, window=0):
                 kk, vv = k[lo:p + 1, h // (heads // kvh)], v[lo:p + 1, h // (heads // kvh)]
                 row = q[cu[b] + i, h]
                 s = kk @ row * scale
+                seen = vs[lo:p + 1, h // (heads // kvh)]
+                vmax = 127 * seen[np.isfinite(seen)].max(initial=0.0)
                 mag = (np.abs(kk) @ np.abs(row)).max() * abs(scale)
                 e = np.exp(s - s.max())
                 l = e.sum()

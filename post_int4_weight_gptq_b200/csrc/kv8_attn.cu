@@ -24,9 +24,9 @@
 // made from S^T's by an 8x8 transpose in registers.
 //
 // Probabilities enter the second product in fp16 as 2^7 p v_scale / (largest
-// v_scale so far), p relative to a running maximum that moves only when a score
-// exceeds it by 2^8: at most 2^15, and what is more than 2^31 below the largest
-// is lost.  The sum of p stays in fp32.
+// v_scale that the row has seen, as a power of two), p relative to a running maximum
+// that moves only when a score exceeds it by 2^7: below 2^15, and what is more than
+// 2^31 below the largest is lost.  The sum of p stays in fp32.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
   __shared__ float s_ks[kMaxPages], s_vs[kMaxPages];
   __shared__ __align__(16) __half s_q[ROWS][D];
   __shared__ float s_rs[ROWS];
-  __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS], s_v[kWarps];
+  __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS], s_d[kWarps][ROWS];
   __shared__ uint64_t full[kWarps][STAGES];
   extern __shared__ uint8_t ring_raw[];  // the warps' rings, then the join's buffer
   uint8_t* const ring = reinterpret_cast<uint8_t*>(
@@ -274,19 +274,18 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
       window > 0 ? max(len - n + static_cast<int>(last_tok) + 1 - window - k0, 0) : 0;
   const int all_hi = row0 + ROWS <= rows ? len - n + static_cast<int>(first_tok) + 1 - k0 : 0;
 
-  float m[NT][2], l[NT][2], o[NT][KS][4];
-  float vmax = 0.0f;
+  float m[NT][2], l[NT][2], vc[NT][2], o[NT][KS][4];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     m[t][0] = m[t][1] = kLow;
     l[t][0] = l[t][1] = 0.0f;
+    vc[t][0] = vc[t][1] = kFirstFactor;
 #pragma unroll
     for (int j = 0; j < KS; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.0f;
   }
 
   int stage = 0;
   const uint32_t mine_at = smem_u32(mine), low = p.low_bytes;
-  float per_vmax = 0.0f;  // 1 / vmax: finite for every scale from 2^-126, kPScale / vmax is not
   uint32_t phase = 0;
   bool ok = true;
   // One step; MASK: some row does not see all of its keys.  Two forms, because the
@@ -337,21 +336,22 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
           }
         }
       }
-    bool over = fmaxf(vscale[0], vscale[1]) > vmax;
+    bool over = false;
+    const float vs_top = fmaxf(fmaxf(vscale[0], vscale[1]), 0.0f);  // (not NaN)
     float top[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         top[t][e] = fmaxf(fmaxf(s[0][t][e], s[0][t][e + 2]), fmaxf(s[1][t][e], s[1][t][e + 2]));
-        over |= top[t][e] > m[t][e] + kSlack;
+        // (a masked row that sees none of the keys, or is none, has no say)
+        over |= top[t][e] > m[t][e] + kSlack ||
+                (vs_top * vc[t][e] >= kWide &&
+                 (!MASK || top[t][e] > __uint_as_float(0xFF800000u)));
       }
     if (__any_sync(0xffffffffu, over)) {
-      // the maximum (or the largest value scale) moves: what was summed is rescaled
-      const float fresh = fmaxf(fmaxf(vscale[0], vscale[1]), vmax);
-      const float fv = vmax > 0.0f ? vmax / fresh : 0.0f;
-      vmax = fresh;
-      per_vmax = vmax > 0.0f ? 1.0f / vmax : 0.0f;
+      // the rows' maxima and factors move (of all rows: each alone moves more often): what
+      // was summed is rescaled
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         float f[2];
@@ -361,11 +361,21 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          const float nm = fmaxf(m[t][e], x);
-          f[e] = exp2_fast(m[t][e] - nm);
-          m[t][e] = nm;
-          l[t][e] *= f[e];
-          f[e] *= fv;
+          float vs = vs_top;
+          if (MASK) {  // of the blocks that the row sees keys of
+            vs = 0.0f;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int k = key0 + 16 * u, h = hi[t][e];
+              if (k < h && (window == 0 || k + 15 >= h - window)) vs = fmaxf(vs, vscale[u]);
+            }
+          }
+          const float by = fminf(m[t][e] - x, 0.0f);
+          const float to = factor_for(vc[t][e], vs);
+          f[e] = exp2_fast(by + static_cast<float>(shift_of(vc[t][e]) - shift_of(to)));
+          l[t][e] *= exp2_fast(by);
+          m[t][e] = by < 0.0f ? x : m[t][e];
+          vc[t][e] = to;
         }
 #pragma unroll
         for (int j = 0; j < KS; ++j) {
@@ -381,16 +391,16 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
     uint32_t pb[2][NT][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const float vf = vscale[u] * per_vmax * kPScale;
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < NT; ++t) {
+        const float vf0 = vscale[u] * vc[t][0], vf1 = vscale[u] * vc[t][1];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float p0 = exp2_fast(s[u][t][2 * h] - m[t][0]);
           const float p1 = exp2_fast(s[u][t][2 * h + 1] - m[t][1]);
           l[t][0] += p0;
           l[t][1] += p1;
-          float y0 = p0 * vf, y1 = p1 * vf;
+          float y0 = p0 * vf0, y1 = p1 * vf1;
           if (MASK) {
             y0 = p0 == 0.0f ? 0.0f : y0;
             y1 = p1 == 0.0f ? 0.0f : y1;
@@ -398,6 +408,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
           const __half2 ph = __floats2half2_rn(y0, y1);
           pb[u][t][h] = transpose8x8(*reinterpret_cast<const uint32_t*>(&ph));
         }
+      }
     }
     // keys past the end of the sequence: their codes are whatever lies there, times 0
 #pragma unroll
@@ -471,10 +482,10 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
       if (r == 0) {
         s_m[warp][8 * t + 2 * c + e] = m[t][e];
         s_l[warp][8 * t + 2 * c + e] = l[t][e];
+        s_d[warp][8 * t + 2 * c + e] = static_cast<float>(shift_of(vc[t][e]));
       }
     }
   }
-  if (lane == 0) s_v[warp] = vmax / kPScale;
   __syncthreads();
   constexpr int PARTS = D / 64;  // threads for a lane's dimensions of one row
   for (int i = threadIdx.x; i < NT * 64 * PARTS; i += 32 * kWarps) {
@@ -482,15 +493,20 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
     const int at = 8 * (te >> 1) + 2 * (src & 3) + (te & 1);  // row of the group
     const int row = row0 + at;
     if (row >= rows) continue;
-    float top = kLow, sum = 0.0f, f[kWarps], x[8] = {};
+    float top = kLow, sum = 0.0f, most = -119.0f, f[kWarps], x[8] = {};
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][at]);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      f[w] = exp2_fast(s_m[w][at] - top);
-      sum += s_l[w][at] * f[w];
-      f[w] *= s_v[w];
+      const float by = s_m[w][at] - top;
+      sum += s_l[w][at] * exp2_fast(by);
+      f[w] = by + s_d[w][at];  // log2 of a warp's sums against 2^7
+      most = fmaxf(most, f[w]);
     }
+    most = ceilf(most);
+    const float undo = undo_factor(static_cast<int>(most));
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) f[w] = exp2_fast(f[w] - most);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
 #pragma unroll
@@ -508,12 +524,12 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
       uint4 v;
       T* w = reinterpret_cast<T*>(&v);
 #pragma unroll
-      for (int d = 0; d < 8; ++d) w[d] = from_float<T>(x[d] * norm);
+      for (int d = 0; d < 8; ++d) w[d] = from_float<T>(x[d] * norm * undo);
       *reinterpret_cast<uint4*>(out + t * p.ldo + head * D + dim) = v;
     } else {
       float4* to = reinterpret_cast<float4*>(p.part_o + slot * D + dim);
-      to[0] = make_float4(x[0], x[1], x[2], x[3]);
-      to[1] = make_float4(x[4], x[5], x[6], x[7]);
+      to[0] = make_float4(x[0] * undo, x[1] * undo, x[2] * undo, x[3] * undo);
+      to[1] = make_float4(x[4] * undo, x[5] * undo, x[6] * undo, x[7] * undo);
     }
     if (sr == 0 && piece == 0) {
       if (!single)

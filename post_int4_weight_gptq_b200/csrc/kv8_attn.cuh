@@ -33,8 +33,27 @@ struct Kv8Attn {
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLow = -3.0e38f;      // below every score: "no key yet"
-constexpr float kPScale = 128.0f;     // 2^7
-constexpr float kSlack = 8.0f;        // log2 by which a score may pass the maximum
+constexpr float kSlack = 7.0f;        // log2 by which a score may pass the maximum
+
+// The weights of the values enter the second product in fp16 as 2^(x - m) v_scale c.
+// c = 2^(7 - d) is a row's own: 2^d is the power of two at or below the largest v_scale
+// of the blocks that the row has seen keys of, so that what a row does not see takes no
+// bits from it (and changes none of them).  d is at least -119 and c a normal number;
+// with scores up to kSlack above the maximum a weight stays below 2^15.
+constexpr float kFirstFactor = 0x1p126f;
+constexpr float kWide = 256.0f;  // v_scale c from which c has to move
+
+// The factor of a row that had c and sees a block of scale vs >= 0.
+__device__ __forceinline__ float factor_for(float c, float vs) {
+  const int d = max(static_cast<int>(__float_as_uint(vs) >> 23) - 127, -119);
+  return fminf(c, __uint_as_float(static_cast<uint32_t>(134 - d) << 23));
+}
+__device__ __forceinline__ int shift_of(float c) {  // d
+  return 134 - static_cast<int>(__float_as_uint(c) >> 23);
+}
+__device__ __forceinline__ float undo_factor(int d) {  // 1 / c = 2^(d - 7)
+  return __uint_as_float(static_cast<uint32_t>(120 + d) << 23);
+}
 
 // The block in which the first key that some query sees lies: chunks are counted
 // from its start.  (Lengths are at most 2^26 and rows below 2^31, so positions are

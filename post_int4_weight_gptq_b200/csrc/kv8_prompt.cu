@@ -6,12 +6,12 @@
 // group share the keys.  Keys pass in tiles of 128:
 //
 //   S = Q K^T    (both fp16 in shared memory; a code is exact in fp16)
-//   P = 2^7 2^(x - m) v_scale / v_max,  x = S scale k_scale   (TMEM over S, fp16)
+//   P = 2^(x - m) v_scale c,  x = S scale k_scale             (TMEM over S, fp16)
 //   O += P V     (P from TMEM, V's codes fp16 in shared memory)
 //
 // with the running maximum m moved, and O rescaled, only when a score passes it
-// by 2^8.  v_max is the largest value scale of the keys in sight, found first;
-// the sum of 2^(x - m) is fp32.  The codes are widened to fp16 as they come from
+// by 2^7.  c is 2^7 over the largest value scale that the row has seen (a power of
+// two, moved like m); the sum of 2^(x - m) is fp32.  The codes are widened to fp16 as they come from
 // the pages (no second copy of the cache exists): bytes go through registers to
 // the swizzled tiles both products read.
 //
@@ -145,9 +145,10 @@ __device__ __forceinline__ float row_max(uint32_t ts, float rs, const float* ks,
 }
 
 // The row's probabilities relative to m, summed into l2, and times the blocks'
-// value factors as halves over the scores.
-__device__ __forceinline__ void row_weights(uint32_t ts, float rs, float m, const float* ks,
-                                            const float* vfs, int from, int upto, uint64_t& l2) {
+// value scales and the row's factor as halves over the scores.
+__device__ __forceinline__ void row_weights(uint32_t ts, float rs, float m, float vc,
+                                            const float* ks, const float* vs, int from, int upto,
+                                            uint64_t& l2) {
   const float ninf = __uint_as_float(0xFF800000u);
   const uint64_t nm2 = pack2(-m, -m);
 #pragma unroll 1
@@ -158,7 +159,7 @@ __device__ __forceinline__ void row_weights(uint32_t ts, float rs, float m, cons
     const uint32_t bits = seen(from, upto, c);
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      const float f = rs * ks[2 * c + g], vf = vfs[2 * c + g];
+      const float f = rs * ks[2 * c + g], vf = vs[2 * c + g] * vc;
       const uint64_t f2 = pack2(f, f), vf2 = pack2(vf, vf);
 #pragma unroll
       for (int i = 16 * g; i < 16 * g + 16; i += 2) {
@@ -169,7 +170,8 @@ __device__ __forceinline__ void row_weights(uint32_t ts, float rs, float m, cons
         const uint64_t e = pack2(exp2_fast(x0), exp2_fast(x1));
         l2 = add2(l2, e);
         unpack2(mul2(e, vf2), y0, y1);
-        // 0 times the scale of a block that holds a NaN is not 0
+        // 0 times the scale of a block that holds a NaN is not 0, nor times one that is
+        // too large for the factor of a row that does not see it
         y0 = (bits >> i) & 1u ? y0 : 0.0f;
         y1 = (bits >> (i + 1)) & 1u ? y1 : 0.0f;
         const __half2 h = __floats2half2_rn(y0, y1);
@@ -233,12 +235,12 @@ __device__ __forceinline__ float part_max(const uint32_t (&s)[32], float rs, con
   return top;
 }
 __device__ __forceinline__ void part_weights(const uint32_t (&s)[32], uint32_t to, float rs,
-                                             uint64_t nm2, const float* ks, const float* vfs,
-                                             uint64_t& la, uint64_t& lb) {
+                                             uint64_t nm2, float vc, const float* ks,
+                                             const float* vs, uint64_t& la, uint64_t& lb) {
   uint32_t w[16];
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    const float f = rs * ks[g], vf = vfs[g];
+    const float f = rs * ks[g], vf = vs[g] * vc;
     const uint64_t f2 = pack2(f, f), vf2 = pack2(vf, vf);
 #pragma unroll
     for (int i = 16 * g; i < 16 * g + 16; i += 2) {
@@ -318,9 +320,9 @@ struct Layout {
 struct Shared {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2];
   uint64_t sc_full[4], q_full, o_done;
-  float ks[4][kGran], vf[4][kGran];  // scales of a tile: a ring of four, so that a slot is
+  float ks[4][kGran], vs[4][kGran];  // scales of a tile: a ring of four, so that a slot is
                                      // rewritten only after both softmaxes have left it
-  int vmax;
+  float vs_top[4];                   // the largest value scale of each (not NaN)
   uint32_t tmem;
 };
 static_assert(sizeof(Shared) <= 1024, "barrier area");
@@ -400,7 +402,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
     for (int i = 0; i < 4; ++i) mbar_init(&sh.sc_full[i], 1);
     mbar_init(&sh.q_full, 4 * nq);
     mbar_init(&sh.o_done, 1);
-    sh.vmax = 0;
     fence_mbar_init();
   }
   if (warp == 12) {
@@ -414,19 +415,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
   // behind the allocation: a kernel that starts early must not hold tensor memory that
   // this one still waits for
   pdl_launch_dependents();
-  // the largest value scale, found by the widening warps
-  auto find_vmax = [&]() {
-    const int b0 = k0 >> shift, b1 = (k1 - 1) >> shift;
-    float top = 0.0f;
-    for (int i = b0 + static_cast<int>(threadIdx.x) - 256; i <= b1; i += 128) {
-      const int pg = __ldg(table + i);
-      if (pg >= 0 && pg < p.pages)
-        top = fmaxf(top, __ldg(p.vs + static_cast<int64_t>(pg) * p.kv_heads + kvh));
-    }
-    top = warp_max(top);
-    if (lane == 0) atomicMax(&sh.vmax, __float_as_int(top));
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-  };
 
   if (warp >= 12) {
     // --------------------------------------------------------------- MMA issuer
@@ -540,9 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
     if (nt > 0) {
       load(p.kc, kr);
       load(p.vc, vr);
-      find_vmax();
     }
-    const float vmax = __int_as_float(sh.vmax);
     for (int j = 0; j < nt; ++j) {
       const int st = j & 1, slot = j & 3;
       const float tks = gks, tvs = gvs;
@@ -550,10 +536,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
       fetch(j + 2);
       if (!wait_warp(&sh.k_empty[st], ((j >> 1) & 1) ^ 1u, p.status, 83)) break;
       if (warp == 8) {
+        float top = fmaxf(tvs, 0.0f);  // lanes l and l + 8 hold the same granule
+#pragma unroll
+        for (int o = 1; o < kGran; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         if (lane < kGran) {
           sh.ks[slot][lane] = tks;
-          sh.vf[slot][lane] = vmax > 0.0f ? kPScale * (tvs / vmax) : (tvs == tvs ? 0.0f : tvs);
+          sh.vs[slot][lane] = tvs;
         }
+        if (lane == 0) sh.vs_top[slot] = top;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.sc_full[slot]);
       }
@@ -591,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
       const int end = len - n + static_cast<int>(rel) + 1;
       const int hi = live ? min(end, c1) : 0;
       const int lo = p.window > 0 ? end - p.window : 0;
-      float m = kLow;
+      float m = kLow, vc = kFirstFactor;
       uint64_t l2 = 0;  // the sum, even and odd keys
       bool ok = true;
       for (int j = 0; j < nt; ++j) {
@@ -603,14 +593,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
         // keys [from, to) of the tile are seen
         const int from = max(lo - key0, 0), upto = min(max(hi - key0, 0), KT);
         const bool mask = __any_sync(0xffffffffu, from > 0 || upto < KT);
-        // The running maximum moves (and O is rescaled) when a score passes it by 2^8.
+        const float *ks = sh.ks[slot], *vs = sh.vs[slot];
+        // The rows' running maxima and factors move (and O is rescaled) when a score passes
+        // one by 2^7 or a row sees keys of a block whose scale is too large for its factor;
+        // those of the whole warp, as each row alone moves more often (298 against 289 us
+        // for two chunks of 2048 tokens behind 2048, 32 heads on 8).
         auto move = [&](float top) {
-          if (!__any_sync(0xffffffffu, top > m + kSlack)) return true;
-          const float nm = fmaxf(m, top);
-          const float f = exp2_fast(m - nm);
-          m = nm;
+          float wide = sh.vs_top[slot];
+          if (!__any_sync(0xffffffffu,
+                          top > m + kSlack || (wide * vc >= kWide && (!mask || upto > from))))
+            return true;
+          if (mask) {
+            wide = 0.0f;
+#pragma unroll 1
+            for (int g = 0; g < kGran; ++g)
+              if (16 * g < upto && 16 * g + 16 > from) wide = fmaxf(wide, vs[g]);
+          }
+          const float by = fminf(m - top, 0.0f), to_c = factor_for(vc, wide);
+          const float f = exp2_fast(by);
+          const float fo = exp2_fast(by + static_cast<float>(shift_of(vc) - shift_of(to_c)));
+          m = by < 0.0f ? top : m;
+          vc = to_c;
           l2 = mul2(l2, pack2(f, f));
-          if (j == 0) return true;
+          if (j == 0 || !__any_sync(0xffffffffu, fo != 1.0f)) return true;
           if (!wait_warp(&sh.pv_done[t], (j - 1) & 1, p.status, 79)) return false;
           tc_fence_after();
 #pragma unroll 1
@@ -619,15 +624,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
             uint32_t w[16];
             tmem_ld_32x32b_x16(to + 16 * c, o);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * f);
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * fo);
             tmem_st_x16(to + 16 * c, w);
           }
           return true;
         };
-        const float *ks = sh.ks[slot], *vf = sh.vf[slot];
         if (mask) {
           if (!(ok = move(row_max(ts, rs, ks, from, upto)))) break;
-          row_weights(ts, rs, m, ks, vf, from, upto, l2);
+          row_weights(ts, rs, m, vc, ks, vs, from, upto, l2);
         } else {
           // two buffers of 32 columns: one is on its way while the other is worked on
           uint32_t sa[32], sb[32];
@@ -652,11 +656,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
 #pragma unroll 1
           for (int c = 0; c < 4; c += 2) {
             tmem_ld_start(ts + 32 * (c + 1), sb);
-            part_weights(sa, ts + 16 * c, rs, nm2, ks + 2 * c, vf + 2 * c, l2, lb);
+            part_weights(sa, ts + 16 * c, rs, nm2, vc, ks + 2 * c, vs + 2 * c, l2, lb);
             tmem_ld_wait();
             tmem_ld_done(sb);
             if (c == 0) tmem_ld_start(ts + 64, sa);
-            part_weights(sb, ts + 16 * c + 16, rs, nm2, ks + 2 * c + 2, vf + 2 * c + 2, l2, lb);
+            part_weights(sb, ts + 16 * c + 16, rs, nm2, vc, ks + 2 * c + 2, vs + 2 * c + 2, l2, lb);
             tmem_ld_wait();
             tmem_ld_done(sa);
           }
@@ -670,11 +674,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
       // ------------------------------------------------------------------- result
       if (ok && nt > 0) ok = wait_warp(&sh.o_done, 0, p.status, 80);
       tc_fence_after();
-      const float vmax = __int_as_float(sh.vmax);
       float la, lb;
       unpack2(l2, la, lb);
       const float l = la + lb;
-      const float norm = (single ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f) * (vmax / kPScale);
+      const float norm = single ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+      const float undo = undo_factor(shift_of(vc));
       const int64_t slot = (static_cast<int64_t>(part) * p.tokens + tok) * p.heads + head;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
@@ -691,15 +695,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
           uint4 v[2];
           T* w = reinterpret_cast<T*>(v);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = from_float<T>(o[i] * norm);
+          for (int i = 0; i < 16; ++i) w[i] = from_float<T>(o[i] * norm * undo);
           reinterpret_cast<uint4*>(at)[0] = v[0];
           reinterpret_cast<uint4*>(at)[1] = v[1];
         } else if (live) {
           float4* at = reinterpret_cast<float4*>(p.part_o + slot * D + 16 * c);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            at[i] = make_float4(o[4 * i] * norm, o[4 * i + 1] * norm, o[4 * i + 2] * norm,
-                                o[4 * i + 3] * norm);
+            at[i] = make_float4(o[4 * i] * undo, o[4 * i + 1] * undo, o[4 * i + 2] * undo,
+                                o[4 * i + 3] * undo);
         }
       }
       if (live) {

@@ -802,7 +802,10 @@ def check_sizes(b, q, news, out, lse, window=0):
     assert worst(np.abs(f64(lse) - rl), tol_l) <= 1
 
 
-@pytest.mark.parametrize("heads,new", [(4, 1), (4, 4)])
+BOTH = [(4, 1), (4, 4), (8, 60)]    # heads and new tokens: groups of rows, tiles of rows
+
+
+@pytest.mark.parametrize("heads,new", BOTH)
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("tiny", [400, 320, 32, 1])
 def test_attention_smallest_value_scales(dim, heads, new, tiny):
@@ -820,3 +823,26 @@ def test_attention_smallest_value_scales(dim, heads, new, tiny):
     q = rand(rng, (new, heads, dim), BF16)
     for max_len in (400, 40000):
         check_sizes(b, q, [new], *run_attention(b, q, [new], max_len))
+
+
+@pytest.mark.parametrize("heads,new", [(4, 4), (8, 60)])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("window", [0, 208])
+@pytest.mark.parametrize("big", [2.0 ** 14, 2.0 ** 40, 2.0 ** 100])
+def test_attention_values_out_of_sight(dim, heads, new, window, big):
+    # Blocks of large values that only some rows see, behind the others' position (no window)
+    # or before their window: the others are as exact as without them, and the same to the bit.
+    rng = np.random.default_rng(dim + window)
+    b = Batch(rng, [386], 1, dim, 16, FP32)
+    k, v = rng.normal(0, 1, (2, 386, 1, dim)).astype(np.float32)
+    large = slice(0, 176) if window else slice(384, 386)
+    v[large] *= big
+    put(b, [386 - new], k[:386 - new], v[:386 - new])
+    put(b, [new], k[386 - new:], v[386 - new:])
+    q = rand(rng, (new, heads, dim), BF16)
+    pos = np.arange(386 - new, 386)
+    blind = (pos - window + 1 >= 176) if window else pos < 384
+    assert 0 < blind.sum() < new
+    for max_len in (386, 40000):
+        out, lse = run_attention(b, q, [new], max_len, window)
+        check_sizes(b, q, [new], out, lse, window)
