@@ -519,17 +519,20 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
     const int64_t t = q0 + tok;
     const int head = kvh * p.group + static_cast<int>(row - tok * p.group);
     const int64_t slot = (static_cast<int64_t>(part) * p.tokens + t) * p.heads + head;
+    // the average before its size: no value on the way is larger than the values are
+    const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int d = 0; d < 8; ++d) x[d] = x[d] * norm * undo;
     if (single) {
-      const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
       uint4 v;
       T* w = reinterpret_cast<T*>(&v);
 #pragma unroll
-      for (int d = 0; d < 8; ++d) w[d] = from_float<T>(x[d] * norm * undo);
+      for (int d = 0; d < 8; ++d) w[d] = from_float<T>(x[d]);
       *reinterpret_cast<uint4*>(out + t * p.ldo + head * D + dim) = v;
     } else {
       float4* to = reinterpret_cast<float4*>(p.part_o + slot * D + dim);
-      to[0] = make_float4(x[0] * undo, x[1] * undo, x[2] * undo, x[3] * undo);
-      to[1] = make_float4(x[4] * undo, x[5] * undo, x[6] * undo, x[7] * undo);
+      to[0] = make_float4(x[0], x[1], x[2], x[3]);
+      to[1] = make_float4(x[4], x[5], x[6], x[7]);
     }
     if (sr == 0 && piece == 0) {
       if (!single)
@@ -541,9 +544,16 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
   }
 }
 
-// Joins the chunks of one (token, head): the largest maximum first, then every
-// warp adds chunks of its own, the loads of several under way at once.
+// Joins the chunks of one (token, head): the largest maximum and the whole sum first,
+// then every warp adds its chunks' averages by their shares of that sum, the loads of
+// several under way at once.
 constexpr int kJoinWarps = 8;
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) kv8_join_kernel(Kv8Attn p) {
@@ -569,18 +579,32 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv8_join_kernel(Kv8Attn p) {
   const int64_t stride = p.tokens * p.heads;
   const float2* ml = p.part_ml + t * p.heads + head;
   const float* po = p.part_o + (t * p.heads + head) * D + V * lane;
-  float top = kLow;
-  for (int i = threadIdx.x; i < nc; i += 32 * kJoinWarps) top = fmaxf(top, ml[i * stride].x);
-  top = warp_max(top);
-  if (lane == 0) s_top[warp] = top;
+  float top = kLow, total = 0.0f;
+  for (int i = threadIdx.x; i < nc; i += 32 * kJoinWarps) {
+    const float2 x = ml[i * stride];
+    const float most = fmaxf(top, x.x);
+    total = total * exp2_fast(top - most) + x.y * exp2_fast(x.x - most);
+    top = most;
+  }
+  const float most = warp_max(top);
+  total = warp_sum(total * exp2_fast(top - most));
+  if (lane == 0) {
+    s_top[warp] = most;
+    s_sum[warp] = total;
+  }
   __syncthreads();
+  top = kLow;
+  total = 0.0f;
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_top[w]);
-  float sum = 0.0f, o[V] = {};
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) total += s_sum[w] * exp2_fast(s_top[w] - top);
+  const float norm = total == 0.0f ? 0.0f : 1.0f / total;
+  float o[V] = {};
 #pragma unroll 4
   for (int i = warp; i < nc; i += kJoinWarps) {
     const float2 x = ml[i * stride];
-    const float f = exp2_fast(x.x - top);
+    const float f = x.y * exp2_fast(x.x - top) * norm;
     const float* at = po + i * stride * D;
     if constexpr (V == 4) {
       const float4 v = *reinterpret_cast<const float4*>(at);
@@ -593,21 +617,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv8_join_kernel(Kv8Attn p) {
       o[0] = fmaf(v.x, f, o[0]);
       o[1] = fmaf(v.y, f, o[1]);
     }
-    sum = fmaf(x.y, f, sum);
   }
-  if (lane == 0) s_sum[warp] = sum;
 #pragma unroll
   for (int j = 0; j < V; ++j) s_o[warp][V * lane + j] = o[j];
   __syncthreads();
-  float total = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) total += s_sum[w];
-  const float norm = total == 0.0f ? 0.0f : 1.0f / total;
   for (int d = threadIdx.x; d < D; d += 32 * kJoinWarps) {
     float x = 0.0f;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) x += s_o[w][d];
-    static_cast<T*>(p.out)[t * p.ldo + head * D + d] = from_float<T>(x * norm);
+    static_cast<T*>(p.out)[t * p.ldo + head * D + d] = from_float<T>(x);
   }
   if (threadIdx.x == 0 && p.lse != nullptr)
     p.lse[t * p.heads + head] =

@@ -24,7 +24,7 @@ struct Kv8Attn {
   void* out;
   int64_t ldo;
   float* lse;
-  float* part_o;   // [chunks][tokens][heads][D] when chunks > 1
+  float* part_o;   // [chunks][tokens][heads][D] when chunks > 1: each chunk's own average
   float2* part_ml; // [chunks][tokens][heads]: running maximum (log2), sum
   int32_t* status;
   uint32_t low_bytes = 0x00FF00FFu;  // a parameter, so that (w & mask) ^ constant is one

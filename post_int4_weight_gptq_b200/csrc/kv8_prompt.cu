@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
       float la, lb;
       unpack2(l2, la, lb);
       const float l = la + lb;
-      const float norm = single ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+      const float norm = l == 0.0f ? 0.0f : 1.0f / l;
       const float undo = undo_factor(shift_of(vc));
       const int64_t slot = (static_cast<int64_t>(part) * p.tokens + tok) * p.heads + head;
 #pragma unroll
@@ -690,20 +690,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[i] = 0.0f;
         }
+        // the average before its size: no value on the way is larger than the values are
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = o[i] * norm * undo;
         if (live && single) {
           T* at = static_cast<T*>(p.out) + tok * p.ldo + head * D + 16 * c;
           uint4 v[2];
           T* w = reinterpret_cast<T*>(v);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = from_float<T>(o[i] * norm * undo);
+          for (int i = 0; i < 16; ++i) w[i] = from_float<T>(o[i]);
           reinterpret_cast<uint4*>(at)[0] = v[0];
           reinterpret_cast<uint4*>(at)[1] = v[1];
         } else if (live) {
           float4* at = reinterpret_cast<float4*>(p.part_o + slot * D + 16 * c);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            at[i] = make_float4(o[4 * i] * undo, o[4 * i + 1] * undo, o[4 * i + 2] * undo,
-                                o[4 * i + 3] * undo);
+            at[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
       }
       if (live) {

@@ -846,3 +846,19 @@ def test_attention_values_out_of_sight(dim, heads, new, window, big):
     for max_len in (386, 40000):
         out, lse = run_attention(b, q, [new], max_len, window)
         check_sizes(b, q, [new], out, lse, window)
+
+
+@pytest.mark.parametrize("heads,new", BOTH)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("size", [1e33, 1e37, 3e38])
+def test_attention_largest_values(dim, heads, new, size):
+    # averages of values near fp32's largest: no sum on the way is larger than they are
+    rng = np.random.default_rng(dim)
+    b = Batch(rng, [1000], 1, dim, 32, FP32)
+    k = rng.normal(0, 0.1, (1000, 1, dim)).astype(np.float32)
+    v = (size * rng.uniform(0.9, 1.0, (1000, 1, dim))).astype(np.float32)
+    put(b, [1000 - new], k[:1000 - new], v[:1000 - new])
+    put(b, [new], k[1000 - new:], v[1000 - new:])
+    q = rand(rng, (new, heads, dim), BF16)
+    for max_len in (1000, 100000):
+        check_sizes(b, q, [new], *run_attention(b, q, [new], max_len))
