@@ -392,6 +392,14 @@ int piq_upper_factor_noalloc(const float* H, int64_t in, float damp, const int32
  * first one staying until the caller clears it; either way no access leaves
  * its buffer, and what depends on the bad value is skipped (writes) or NaN
  * (results). */
+
+/* Every wait inside these kernels (for a copy, a product, another warp) gives up
+ * after 2 s, which is PIQ_ERR_TIMEOUT in `status`.  This sets the limit of the
+ * calls made from now on in this process (a captured graph keeps the one it was
+ * captured with): 1 .. 10^10 ns, 0 for the 2 s.  For tests of what happens then;
+ * host only. */
+int piq_serving_wait_limit(uint64_t wait_ns);
+
 enum piq_dtype { PIQ_BF16 = 0, PIQ_FP16 = 1, PIQ_FP32 = 2 };
 
 /* Rows to int8, one scale a row: the tokens of X, or the output channels of W.

@@ -105,6 +105,7 @@ SIGNATURES = {
                                    _vp]),
     "piq_upper_factor_noalloc": (_c_int, [_vp, _c_i64, _c_float, _vp, _vp,
                                           ctypes.POINTER(ctypes.c_double), _vp]),
+    "piq_serving_wait_limit": (_c_int, [ctypes.c_uint64]),
     "piq_int8_quantize_rows": (_c_int, [_vp, _c_int, _c_i64, _c_i64, _c_i64, _vp, _c_i64, _vp,
                                         _vp]),
     "piq_int8_linear_workspace_bytes": (_c_int, [_c_i64, _c_i64, _c_i64, _c_size_p]),
@@ -559,6 +560,12 @@ def check_status(status, where="8-bit call"):
     if code != PIQ_OK:
         status.zero_()
         raise PiqError(code, where)
+
+
+def serving_wait_limit(wait_ns=0):
+    """Limit, in ns, of the waits inside the 8-bit kernels of later calls (0: the
+    usual 2 s): a diagnostic, for tests of what a wait that gives up leaves."""
+    _check(load_library().piq_serving_wait_limit(wait_ns), "piq_serving_wait_limit")
 
 
 def int8_quantize_rows(X, stream=None):

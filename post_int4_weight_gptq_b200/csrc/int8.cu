@@ -8,6 +8,7 @@
 // the order or the split of the sum; the scales and the bias are applied in
 // fp32 and the value is rounded once to Y's type.
 #include <algorithm>
+#include <atomic>
 
 #include "serve.h"
 
@@ -243,16 +244,27 @@ LinearWs linear_ws(int64_t tokens, int64_t in) {
   return w;
 }
 
+std::atomic<uint64_t> g_wait_ns{kWaitLimitNs};
+
 bool linear_sizes_ok(int64_t tokens, int64_t out, int64_t in) {
   return tokens >= 0 && tokens <= (int64_t)1 << 30 && out >= 1 && out <= (int64_t)1 << 24 &&
          in >= 8 && in % 8 == 0 && in <= kInt8MaxIn;
 }
 
 }  // namespace
+
+uint64_t serving_wait_ns() { return g_wait_ns.load(std::memory_order_relaxed); }
+
 }  // namespace piq
 
 extern "C" {
 using namespace piq;
+
+int piq_serving_wait_limit(uint64_t wait_ns) {
+  if (wait_ns > 10000000000ull) return PIQ_ERR_INVALID_ARG;
+  g_wait_ns.store(wait_ns == 0 ? kWaitLimitNs : wait_ns, std::memory_order_relaxed);
+  return PIQ_OK;
+}
 
 int piq_int8_quantize_rows(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ldx,
                            int8_t* codes, int64_t ldc, float* scales, void* stream) {

@@ -54,6 +54,7 @@ struct GemmArgs {
   int64_t ldy;
   bool wide;  // Y and its rows are 16-byte aligned
   int32_t* status;
+  uint64_t wait_ns;  // limit of a wait
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -75,6 +76,9 @@ __device__ __forceinline__ int4 ld_cluster(uint32_t addr) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "r"(addr));
   return v;
+}
+__device__ __forceinline__ void st_cluster_word(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
@@ -145,6 +149,14 @@ __device__ __forceinline__ void store_tokens(const GemmArgs& p, T* stage, const 
   __syncwarp();
 }
 
+// NaN for tokens [t0, t0 + n) of channel c, behind a wait that gave up.
+template <typename T>
+__device__ __forceinline__ void store_nan(const GemmArgs& p, int t0, int n, int c) {
+  if (c >= p.out) return;
+  for (int t = t0; t < min(t0 + n, p.tokens); ++t)
+    static_cast<T*>(p.Y)[t * p.ldy + c] = from_float<T>(__uint_as_float(0x7FC00000u));
+}
+
 // ------------------------------------------------------------------- split
 template <typename T, int NT>
 __global__ void __launch_bounds__(192, NT <= 64 ? 2 : 1)
@@ -160,8 +172,10 @@ __global__ void __launch_bounds__(192, NT <= 64 ? 2 : 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + RING);
   uint64_t* empty = full + STAGES;
   uint64_t* done = empty + STAGES;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* drain = done + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   __shared__ __align__(16) float s_sx[NT];
+  __shared__ uint32_t s_bad;  // a wait of this CTA gave up
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slices = p.slices, slice = blockIdx.x % slices;  // a cluster is one tile's slices
   const int c0 = blockIdx.x / slices * BM, t0 = blockIdx.y * NT;
@@ -175,6 +189,8 @@ __global__ void __launch_bounds__(192, NT <= 64 ? 2 : 1)
       mbar_init(&empty[s], 1);
     }
     mbar_init(done, 1);
+    mbar_init(drain, 1);
+    s_bad = 0;
     fence_mbar_init();
     // The weights do not depend on the kernel before this one, which lets this
     // one start only after the one before that is complete: the ring fills with
@@ -196,12 +212,17 @@ __global__ void __launch_bounds__(192, NT <= 64 ? 2 : 1)
   pdl_wait();
   pdl_launch_dependents();
 
+  int copies = 0;      // steps whose copies the copying thread has asked for
+  bool began = false;  // the issuing thread has issued products
   if (warp == 0) {
     if (lane == 0) {
-      for (int kb = kb0; kb < kb1; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb, ++copies) {
         const int it = kb - kb0, st = it % STAGES;
         if (it >= STAGES) {
-          if (!wait_bar(&empty[st], ((it / STAGES) & 1) ^ 1u, p.status, 61)) break;
+          if (!wait_bar(&empty[st], ((it / STAGES) & 1) ^ 1u, p.wait_ns, p.status, 61)) {
+            s_bad = 1;
+            break;
+          }
           mbar_arrive_expect_tx(&full[st], STAGE);
           tma_load_2d(smem + st * STAGE, &tmW, &full[st], kb * BK, c0);
         }
@@ -213,10 +234,12 @@ __global__ void __launch_bounds__(192, NT <= 64 ? 2 : 1)
       bool ok = true;
       for (int kb = kb0; kb < kb1; ++kb) {
         const int it = kb - kb0, st = it % STAGES;
-        if (!wait_bar(&full[st], (it / STAGES) & 1, p.status, 62)) {
+        if (!wait_bar(&full[st], (it / STAGES) & 1, p.wait_ns, p.status, 62)) {
           ok = false;
+          s_bad = 1;
           break;
         }
+        began = true;
         tc_fence_after();
         const uint32_t a = smem_u32(smem + st * STAGE);
         const uint64_t ad = smem_desc(a, 16, 1024, kLayoutSw128);
@@ -238,7 +261,7 @@ __global__ void __launch_bounds__(192, NT <= 64 ? 2 : 1)
     for (int i = threadIdx.x - 64; i < NT; i += 128)
       s_sx[i] = __ldg(p.sx + min(t0 + i, p.tokens - 1));
     asm volatile("bar.sync 1, 128;" ::: "memory");
-    const bool ok = wait_warp(done, 0, p.status, 63);
+    const bool ok = wait_warp(done, 0, p.wait_ns, p.status, 63);
     tc_fence_after();
     // the ring is empty now: staging of the stores, or this slice's sums [NT][BM]
     constexpr int CH = NT < 32 ? NT : 32;
@@ -259,10 +282,25 @@ __global__ void __launch_bounds__(192, NT <= 64 ? 2 : 1)
           for (int i = 0; i < CH; ++i) part[(n + i) * BM + ch] = __float_as_int(f[i]);
         }
       }
+    } else {
+      s_bad = 1;
     }
   }
   tc_fence_before();
   __syncthreads();
+  if (s_bad) {
+    // what is under way ends before anyone reads the ring or leaves: the last copies into
+    // every stage (of each step both tiles were asked for), and the products
+    if (warp == 0 && lane == 0) {
+      const uint64_t now = global_timer_ns();
+      for (int it = max(copies - STAGES, 0); it < copies; ++it)
+        drain_bar(&full[it % STAGES], (it / STAGES) & 1, now);
+    } else if (warp == 1 && lane == 0 && began) {
+      umma_commit(drain);
+      drain_bar(drain, 0, global_timer_ns());
+    }
+    __syncthreads();
+  }
   if (slices > 1) {
     cluster_sync();
     // this CTA's share of the tokens: a warp a token, four channels a lane, every
@@ -311,6 +349,8 @@ __global__ void __launch_bounds__(192, NT <= 64 ? 2 : 1)
     }
     cluster_sync();  // nobody leaves while its part is read
   }
+  // this slice is missing in what the cluster has stored
+  if (s_bad && warp >= 2) store_nan<T>(p, t0, NT, c0 + (warp & 3) * 32 + lane);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, COLS);
@@ -349,6 +389,20 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
       : "memory");
 }
 
+// The same on this CTA's `bar` alone.
+__device__ __forceinline__ void umma_commit_pair_here(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+// `bytes` that no copy will bring are taken off the current phase of `bar`.
+__device__ __forceinline__ void mbar_forgo_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+               "r"(bytes)
+               : "memory");
+}
+
 template <typename T, int NT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpi, 1)
     int8_pair_kernel(const __grid_constant__ CUtensorMap tmW,
@@ -362,7 +416,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpi, 1)
   uint64_t* empty = full + STAGES;
   uint64_t* acc_full = empty + STAGES;  // [2]
   uint64_t* acc_empty = acc_full + 2;   // [2], the first CTA's counts both CTAs' warps
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  __shared__ uint32_t s_bad;        // a wait of either CTA gave up
+  __shared__ uint32_t s_copies[2];  // steps whose copies each CTA has asked for
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -378,6 +435,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpi, 1)
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 2 * kEpi);
     }
+    mbar_init(drain, 1);
+    s_bad = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmX);
@@ -396,7 +455,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpi, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
   pdl_launch_dependents();
+  auto gave_up = [&]() {  // both CTAs know it behind the barrier at the end
+    for (uint32_t r = 0; r < 2; ++r) st_cluster_word(map_rank(smem_u32(&s_bad), r), 1);
+  };
 
+  bool began = false;  // the issuing thread has issued products
   if (warp == 0) {
     if (lane == 0) {
       const uint32_t full0 = map_rank(smem_u32(full), 0);
@@ -409,8 +472,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpi, 1)
         const int t0 = n * NT + static_cast<int>(rank) * (NT / 2);
         for (int kb = 0; kb < num_kb; ++kb, ++it) {
           const int st = it % STAGES;
-          if (!wait_bar(&empty[st], ((it / STAGES) & 1) ^ 1u, p.status, 64)) {
+          if (!wait_bar(&empty[st], ((it / STAGES) & 1) ^ 1u, p.wait_ns, p.status, 64)) {
             ok = false;
+            gave_up();
             break;
           }
           if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * STAGE);
@@ -418,6 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpi, 1)
           tma_load_2d_pair(smem + st * STAGE + A_TILE, &tmX, full0 + 8 * st, kb * BK, t0);
         }
       }
+      for (uint32_t r = 0; r < 2; ++r) st_cluster_word(map_rank(smem_u32(&s_copies[rank]), r), it);
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
@@ -426,14 +491,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpi, 1)
       bool ok = true;
       for (int t = pair; t < tiles && ok; t += pairs, ++lt) {
         const int buf = lt & 1;
-        if (!wait_bar(&acc_empty[buf], ((lt >> 1) & 1) ^ 1u, p.status, 65)) break;
+        if (!wait_bar(&acc_empty[buf], ((lt >> 1) & 1) ^ 1u, p.wait_ns, p.status, 65)) {
+          gave_up();
+          break;
+        }
         tc_fence_after();
         for (int kb = 0; kb < num_kb; ++kb, ++it) {
           const int st = it % STAGES;
-          if (!wait_bar(&full[st], (it / STAGES) & 1, p.status, 66)) {
+          if (!wait_bar(&full[st], (it / STAGES) & 1, p.wait_ns, p.status, 66)) {
             ok = false;
+            gave_up();
             break;
           }
+          began = true;
           tc_fence_after();
           const uint32_t a = smem_u32(smem + st * STAGE);
           const uint64_t ad = smem_desc(a, 16, 1024, kLayoutSw128);
@@ -452,6 +522,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpi, 1)
     const uint32_t free_bar = map_rank(smem_u32(acc_empty), 0);
     T* const stage = reinterpret_cast<T*>(smem + kRing + 1024) + (warp - 2) * (32 * 32);
     int lt = 0;
+    bool ok = true;
     for (int t = pair; t < tiles; t += pairs, ++lt) {
       int m, n;
       pair_tile(p, t, m, n);
@@ -459,9 +530,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpi, 1)
       const int c = (2 * m + static_cast<int>(rank)) * BM + q * 32 + lane;
       const float sw = c < p.out ? __ldg(p.sw + c) : 0.0f;
       const float bias = p.bias != nullptr && c < p.out ? __ldg(p.bias + c) : 0.0f;
-      if (!wait_warp(&acc_full[buf], (lt >> 1) & 1, p.status, 67)) break;
-      tc_fence_after();
       const int t0 = n * NT + h * (NT / 2);
+      if (ok && !wait_warp(&acc_full[buf], (lt >> 1) & 1, p.wait_ns, p.status, 67)) {
+        ok = false;
+        if (lane == 0) gave_up();
+      }
+      if (!ok) {  // this tile and those after it
+        store_nan<T>(p, t0, NT / 2, c);
+        continue;
+      }
+      tc_fence_after();
       const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * NT + h * (NT / 2);
       for (int i0 = 0; i0 < NT / 2 && t0 + i0 < p.tokens; i0 += 32) {
         float f[32];
@@ -490,6 +568,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpi, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // no arrival or load of the pair is under way when a CTA leaves
+  if (s_bad) {  // in both CTAs
+    // After a wait that gave up some are.  The first CTA holds the barriers: it waits for
+    // its products, and for the last copies of both into every stage, where one may have
+    // gone a few steps further than the other.
+    if (rank == 0 && warp == 1 && lane == 0 && began) {
+      umma_commit_pair_here(drain);
+      drain_bar(drain, 0, global_timer_ns());
+    } else if (rank == 0 && warp == 0 && lane == 0) {
+      const uint64_t now = global_timer_ns();
+      const int mine = s_copies[0], other = s_copies[1], all = max(mine, other);
+      for (int it = max(all - STAGES, 0); it < all; ++it) {
+        uint64_t* const bar = &full[it % STAGES];
+        if (it >= mine)
+          mbar_arrive_expect_tx(bar, STAGE);  // only the other's
+        else if (it >= other)
+          mbar_forgo_tx(bar, STAGE);          // only this one's
+        drain_bar(bar, (it / STAGES) & 1, now);
+      }
+    }
+    __syncthreads();
+    cluster_sync();
+  }
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * NT)
@@ -661,6 +761,7 @@ int launch_int8_gemm(const int8_t* qx, int64_t ldq, const float* sx, int64_t tok
   const int size = dtype == PIQ_FP32 ? 4 : 2;
   p.wide = ptr_aligned(Y, 16) && ldy * size % 16 == 0;
   p.status = status;
+  p.wait_ns = serving_wait_ns();
   switch (dtype) {
     case PIQ_BF16: return gemm_t<__nv_bfloat16>(qx, ldq, W, ldw, p, stream, info.sm_count);
     case PIQ_FP16: return gemm_t<__half>(qx, ldq, W, ldw, p, stream, info.sm_count);

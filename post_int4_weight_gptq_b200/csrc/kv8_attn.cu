@@ -445,9 +445,10 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
       }
     }
   };
+  int step = warp;
 #pragma unroll 1
-  for (int step = warp; step < steps; step += kWarps) {
-    if (!(ok = wait_warp(&full[warp][stage], phase, p.status, 91))) break;
+  for (; step < steps; step += kWarps) {
+    if (!(ok = wait_warp_short(&full[warp][stage], phase, p.wait_ns, p.status, 91))) break;
     if (32 * step < all_lo || 32 * step + 32 > all_hi)
       process(step, std::true_type());
     else
@@ -459,6 +460,17 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
       stage = 0;
       phase ^= 1u;
     }
+  }
+
+  if (!ok) {
+    // The copies under way end before the rings are written over, and the rows are NaN.
+    const uint64_t t0 = global_timer_ns();
+    for (int i = 0; i < STAGES && step + i * kWarps < steps; ++i) {
+      const int s = stage + i;
+      drain_bar(&full[warp][s % STAGES], s < STAGES ? phase : phase ^ 1u, t0);
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) l[t][0] = l[t][1] = __uint_as_float(0x7FC00000u);
   }
 
   // --------------------------------------------------------------- join the warps
@@ -842,6 +854,7 @@ int piq_kv8_attention(const void* q, int dtype, int64_t tokens, int64_t ldq, int
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + w.ml_at);
   p.status = status;
+  p.wait_ns = serving_wait_ns();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == PIQ_BF16)
     return head_dim == 128 ? launch_attention<__nv_bfloat16, 128>(p, a, s)

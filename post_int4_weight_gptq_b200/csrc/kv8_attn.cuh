@@ -27,6 +27,7 @@ struct Kv8Attn {
   float* part_o;   // [chunks][tokens][heads][D] when chunks > 1: each chunk's own average
   float2* part_ml; // [chunks][tokens][heads]: running maximum (log2), sum
   int32_t* status;
+  uint64_t wait_ns;  // limit of a wait
   uint32_t low_bytes = 0x00FF00FFu;  // a parameter, so that (w & mask) ^ constant is one
                                      // instruction: with two literals it became two
 };

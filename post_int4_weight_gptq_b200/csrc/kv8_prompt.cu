@@ -319,7 +319,7 @@ struct Layout {
 
 struct Shared {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2];
-  uint64_t sc_full[4], q_full, o_done;
+  uint64_t sc_full[4], q_full, o_done, drain;
   float ks[4][kGran], vs[4][kGran];  // scales of a tile: a ring of four, so that a slot is
                                      // rewritten only after both softmaxes have left it
   float vs_top[4];                   // the largest value scale of each (not NaN)
@@ -402,6 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
     for (int i = 0; i < 4; ++i) mbar_init(&sh.sc_full[i], 1);
     mbar_init(&sh.q_full, 4 * nq);
     mbar_init(&sh.o_done, 1);
+    mbar_init(&sh.drain, 1);
     fence_mbar_init();
   }
   if (warp == 12) {
@@ -432,7 +433,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
         }
         umma_commit(&sh.s_full[t]);
       };
-      bool ok = wait_bar(&sh.q_full, 0, p.status, 70) && wait_bar(&sh.k_full[0], 0, p.status, 71);
+      bool ok = wait_bar(&sh.q_full, 0, p.wait_ns, p.status, 70) && wait_bar(&sh.k_full[0], 0, p.wait_ns, p.status, 71);
+      const bool began = ok;
       if (ok) {
         tc_fence_after();
         for (int t = 0; t < nq; ++t) scores(t, 0);
@@ -440,11 +442,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
       }
       for (int j = 0; j < nt && ok; ++j) {
         const int st = j & 1;
-        if (!(ok = wait_bar(&sh.v_full[st], (j >> 1) & 1, p.status, 72))) break;
+        if (!(ok = wait_bar(&sh.v_full[st], (j >> 1) & 1, p.wait_ns, p.status, 72))) break;
         const bool more = j + 1 < nt;
-        if (more && !(ok = wait_bar(&sh.k_full[st ^ 1], ((j + 1) >> 1) & 1, p.status, 73))) break;
+        if (more && !(ok = wait_bar(&sh.k_full[st ^ 1], ((j + 1) >> 1) & 1, p.wait_ns, p.status, 73))) break;
         for (int t = 0; t < nq; ++t) {
-          if (!(ok = wait_bar(&sh.p_full[t], j & 1, p.status, 74))) break;
+          if (!(ok = wait_bar(&sh.p_full[t], j & 1, p.wait_ns, p.status, 74))) break;
           tc_fence_after();
           const uint32_t v = qa + L::V_AT + st * L::TILE;
 #pragma unroll
@@ -456,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
           if (more) {
             // The next scores go over the P that this product reads: MMAs on other
             // accumulators are not ordered behind it, so its end is waited for.
-            if (!(ok = wait_bar(&sh.pv_done[t], j & 1, p.status, 76))) break;
+            if (!(ok = wait_bar(&sh.pv_done[t], j & 1, p.wait_ns, p.status, 76))) break;
             scores(t, st ^ 1);
           }
         }
@@ -464,10 +466,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
         umma_commit(&sh.v_empty[st]);
         if (more) umma_commit(&sh.k_empty[st ^ 1]);
       }
-      // the end of everything; the arrival is in before the barrier's memory goes
-      if (ok) {
-        umma_commit(&sh.o_done);
-        wait_bar(&sh.o_done, 0, p.status, 81);
+      // the end of everything; the arrival is in before the barrier's memory goes.  After a
+      // wait that gave up, the same on a barrier that tells nobody that O is there.
+      if (began) {
+        uint64_t* const end = ok ? &sh.o_done : &sh.drain;
+        umma_commit(end);
+        drain_bar(end, 0, global_timer_ns());
       }
     }
   } else if (warp >= 8) {
@@ -534,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
       const float tks = gks, tvs = gvs;
       look(j + 1);
       fetch(j + 2);
-      if (!wait_warp(&sh.k_empty[st], ((j >> 1) & 1) ^ 1u, p.status, 83)) break;
+      if (!wait_warp(&sh.k_empty[st], ((j >> 1) & 1) ^ 1u, p.wait_ns, p.status, 83)) break;
       if (warp == 8) {
         float top = fmaxf(tvs, 0.0f);  // lanes l and l + 8 hold the same granule
 #pragma unroll
@@ -552,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.k_full[st]);
       if (j + 1 < nt) load(p.kc, kr);
-      if (!wait_warp(&sh.v_empty[st], ((j >> 1) & 1) ^ 1u, p.status, 84)) break;
+      if (!wait_warp(&sh.v_empty[st], ((j >> 1) & 1) ^ 1u, p.wait_ns, p.status, 84)) break;
       store(smem + L::V_AT + st * L::TILE, vr);
       fence_proxy_async_smem();
       __syncwarp();
@@ -587,8 +591,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
       for (int j = 0; j < nt; ++j) {
         const int slot = j & 3;
         const int key0 = k0 + j * KT;
-        if (!(ok = wait_warp(&sh.sc_full[slot], (j >> 2) & 1, p.status, 77))) break;
-        if (!(ok = wait_warp(&sh.s_full[t], j & 1, p.status, 78))) break;
+        if (!(ok = wait_warp(&sh.sc_full[slot], (j >> 2) & 1, p.wait_ns, p.status, 77))) break;
+        if (!(ok = wait_warp(&sh.s_full[t], j & 1, p.wait_ns, p.status, 78))) break;
         tc_fence_after();
         // keys [from, to) of the tile are seen
         const int from = max(lo - key0, 0), upto = min(max(hi - key0, 0), KT);
@@ -616,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
           vc = to_c;
           l2 = mul2(l2, pack2(f, f));
           if (j == 0 || !__any_sync(0xffffffffu, fo != 1.0f)) return true;
-          if (!wait_warp(&sh.pv_done[t], (j - 1) & 1, p.status, 79)) return false;
+          if (!wait_warp(&sh.pv_done[t], (j - 1) & 1, p.wait_ns, p.status, 79)) return false;
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D / 16; ++c) {
@@ -672,11 +676,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
         if (lane == 0) mbar_arrive(&sh.p_full[t]);
       }
       // ------------------------------------------------------------------- result
-      if (ok && nt > 0) ok = wait_warp(&sh.o_done, 0, p.status, 80);
+      if (ok && nt > 0) ok = wait_warp(&sh.o_done, 0, p.wait_ns, p.status, 80);
       tc_fence_after();
       float la, lb;
       unpack2(l2, la, lb);
-      const float l = la + lb;
+      const float l = ok ? la + lb : __uint_as_float(0x7FC00000u);
       const float norm = l == 0.0f ? 0.0f : 1.0f / l;
       const float undo = undo_factor(shift_of(vc));
       const int64_t slot = (static_cast<int64_t>(part) * p.tokens + tok) * p.heads + head;
@@ -684,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
       for (int c = 0; c < D / 16; ++c) {
         float o[16];
         __syncwarp();
-        if (nt > 0) {
+        if (ok && nt > 0) {
           tmem_ld_32x32b_x16(to + 16 * c, o);
         } else {
 #pragma unroll

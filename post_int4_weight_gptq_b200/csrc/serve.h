@@ -31,11 +31,16 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn tensor_map_encoder();
 
-// A bounded wait that reports to the caller's status words.  Without mbar_wait's
-// suspend hint, as these kernels' waits are short (the prompt kernel took 406 us
-// without and 414 with it, next to nothing).
+// The limit of the waits inside the kernels launched from now on
+// (piq_serving_wait_limit).
+uint64_t serving_wait_ns();
+
+// A wait bounded by `limit` ns that reports to the caller's status words.  Who gives up
+// makes the results that depend on the wait NaN, and no CTA ends with copies or products
+// of its own under way: those are waited for with drain_bar.  Without mbar_wait's
+// suspend hint, as these waits are short.
 __device__ __forceinline__ void note_status(int32_t* status, int code, int detail);
-__device__ __forceinline__ bool try_wait_now(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool try_wait_now(uint64_t* bar, uint32_t parity) {  // may sleep
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -46,23 +51,58 @@ __device__ __forceinline__ bool try_wait_now(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int32_t* status,
-                                         int where) {
+__device__ __forceinline__ bool test_now(uint64_t* bar, uint32_t parity) {  // does not
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+constexpr uint64_t kBriefNs = 1000000;  // limits below it look at the clock every time
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, uint64_t limit,
+                                         int32_t* status, int where) {
   if (try_wait_now(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
+  const int tries = limit < kBriefNs ? 1 : 64;
   for (;;) {
-    for (int i = 0; i < 64; ++i)
+    for (int i = 0; i < tries; ++i)
       if (try_wait_now(bar, parity)) return true;
-    if (global_timer_ns() - t0 > kWaitLimitNs) {
+    if (global_timer_ns() - t0 >= limit) {
       note_status(status, PIQ_ERR_TIMEOUT, where);
       return false;
     }
   }
 }
 // The same for a whole warp, which goes on or gives up together.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int32_t* status,
-                                          int where) {
-  return __all_sync(0xffffffffu, wait_bar(bar, parity, status, where));
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint64_t limit,
+                                          int32_t* status, int where) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, limit, status, where));
+}
+// For waits so short that one sleeping try outlasts them, whatever the limit: below
+// kBriefNs without sleeping.
+__device__ __forceinline__ bool wait_warp_short(uint64_t* bar, uint32_t parity, uint64_t limit,
+                                                int32_t* status, int where) {
+  bool ok = test_now(bar, parity);
+  if (!ok) {
+    if (limit >= kBriefNs) {
+      ok = wait_bar(bar, parity, limit, status, where);
+    } else {
+      const uint64_t t0 = global_timer_ns();
+      while (!(ok = test_now(bar, parity)) && global_timer_ns() - t0 < limit) {
+      }
+      if (!ok) note_status(status, PIQ_ERR_TIMEOUT, where);
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+// Waits, up to kWaitLimitNs from t0 on, for what is under way and will arrive on `bar`.
+__device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity, uint64_t t0) {
+  while (!try_wait_now(bar, parity) && global_timer_ns() - t0 < kWaitLimitNs) {
+  }
 }
 
 inline bool ptr_aligned(const void* p, uintptr_t a) {

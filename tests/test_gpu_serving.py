@@ -862,3 +862,63 @@ def test_attention_largest_values(dim, heads, new, size):
     q = rand(rng, (new, heads, dim), BF16)
     for max_len in (1000, 100000):
         check_sizes(b, q, [new], *run_attention(b, q, [new], max_len))
+
+
+# ---------------------------------------------------------------- waits that give up
+def linear_call(tokens, inp, out):
+    rng = np.random.default_rng(tokens)
+    x, w, ws, bias = linear_case(rng, tokens, inp, out, BF16, True)
+    y = torch.empty(tokens, out, dtype=BF16, device="cuda")
+    return lambda status: (piq.int8_linear(x, w, ws, bias, out=y, status=status),)
+
+
+def attention_call(heads, kv_heads, dim, batch, new, length, max_len):
+    g = torch.Generator(device="cuda").manual_seed(heads)
+    pages = -(-length // 64)
+    shape = (batch * pages, kv_heads, 64, dim)
+    codes = [torch.randint(-127, 128, shape, generator=g, device="cuda", dtype=torch.int8)
+             for _ in range(2)]
+    scales = [torch.rand(shape[:2], generator=g, device="cuda") / 50 for _ in range(2)]
+    cache = piq.KV8Cache(*codes, *scales)
+    table = torch.randperm(shape[0], generator=g, device="cuda").int().view(batch, pages)
+    q = torch.randn(batch * new, heads, dim, generator=g, device="cuda").to(BF16)
+    cu, lens = ints([new * i for i in range(batch + 1)]), ints([length] * batch)
+    return lambda status: piq.kv8_attention(cache, q, cu, lens, table, new, max_len,
+                                            return_lse=True, status=status)
+
+
+@pytest.mark.parametrize("call,args", [
+    (linear_call, (300, 1032, 2050)),            # one slice of k
+    (linear_call, (37, 11008, 4096)),            # eight, joined in a cluster
+    (linear_call, (2100, 4104, 4000)),           # pairs of CTAs, several tiles each
+    (attention_call, (32, 8, 128, 32, 1, 4096, 4096)),      # groups of rows
+    (attention_call, (16, 8, 64, 4, 1, 50000, 50000)),    # split and joined
+    (attention_call, (32, 2, 128, 4, 300, 2000, 2000)),     # tiles of rows
+    (attention_call, (8, 1, 64, 2, 60, 3000, 60000))])      # split and joined
+def test_a_wait_that_gives_up_leaves_nan(call, args):
+    # the shortest limit: what a wait was given up for is NaN, the rest as it should be, the
+    # status says so, and the next call is what it was
+    run = call(*args)
+    want, status = [t.clone() for t in run(None)], piq.new_status()
+    seen = 0
+    try:
+        for _ in range(5):
+            status.zero_()
+            piq.serving_wait_limit(1)
+            got = run(status)
+            torch.cuda.synchronize()
+            piq.serving_wait_limit(0)
+            code = status.tolist()[0]
+            assert code in (piq.PIQ_OK, piq.PIQ_ERR_TIMEOUT)
+            seen += code != piq.PIQ_OK
+            for g, w in zip(got, want):
+                nan = torch.isnan(g)
+                assert torch.equal(g[~nan], w[~nan])
+                assert code == piq.PIQ_ERR_TIMEOUT or not nan.any()
+    finally:
+        piq.serving_wait_limit(0)
+    assert seen
+    status.zero_()
+    for g, w in zip(run(status), want):
+        assert torch.equal(g, w)
+    assert status.tolist() == [0, 0]

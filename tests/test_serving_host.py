@@ -209,3 +209,9 @@ def test_oracle_attention_against_a_plain_softmax():
         p = np.exp(s)
         assert np.allclose(out[i], p @ v[:18 + i] / p.sum(1, keepdims=True), rtol=1e-12)
         assert np.allclose(lse[i], np.log(p.sum(1)), rtol=1e-12)
+
+
+def test_wait_limit(lib):
+    assert lib.piq_serving_wait_limit(10 ** 10 + 1) == piq.PIQ_ERR_INVALID_ARG
+    for ns in (1, 10 ** 10, 0):
+        piq.serving_wait_limit(ns)
