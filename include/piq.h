@@ -442,6 +442,8 @@ int piq_int8_linear(const void* X, int dtype, int64_t tokens, int64_t in, int64_
  * 1 <= batch <= 65535; 1 <= pages, pages * kv_heads < 2^31. Rows of ragged tensors belong to
  * sequences by cu (device int32 [batch + 1], non-decreasing): rows cu[b] ..
  * cu[b + 1] - 1 are sequence b's, in order; rows of no sequence are not touched.
+ * (Rows below 0, behind the tensor or in decreasing order are an error of that
+ * sequence: it is not written, or what rows it has are NaN.)
  *
  * piq_kv8_append quantizes new tokens as it writes them.  Sequence b has
  * lens_before[b] tokens in the cache and gets the rows cu_new[b] .. of k and v

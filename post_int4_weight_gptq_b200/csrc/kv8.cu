@@ -69,16 +69,24 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(Kv8Write p) {
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int head = blockIdx.y;
+  auto bad = [&](int64_t row0, int64_t row1, int64_t before) {
+    return bad_rows(row0, row1, p.tokens) ||
+           (row0 != row1 && (before < 0 || before + (row1 - row0) > p.width * p.block));
+  };
+  // Bad lengths are reported by a CTA of its own (one item more than there can be), for the
+  // whole batch: with starts that cannot be, the search may pass a sequence by.
+  if (blockIdx.x == gridDim.x - 1) {
+    if (head == 0 && blockIdx.z == 0)
+      for (int i = threadIdx.x; i < p.batch; i += blockDim.x)
+        if (bad(__ldg(p.cu + i), __ldg(p.cu + i + 1), __ldg(p.lens + i)))
+          note_status(p.status, PIQ_ERR_INVALID_ARG, i);
+    return;
+  }
   const int b = find_item(p.cu, p.batch, p.block, blockIdx.x, lane);
   if (b < 0) return;
   const int64_t row0 = __ldg(p.cu + b), row1 = __ldg(p.cu + b + 1);
   const int64_t before = __ldg(p.lens + b);
-  if (row0 == row1) return;
-  if (row0 < 0 || row1 < row0 || row1 > p.tokens || before < 0 ||
-      before + (row1 - row0) > p.width * p.block) {
-    if (threadIdx.x == 0) note_status(p.status, PIQ_ERR_INVALID_ARG, b);
-    return;
-  }
+  if (row0 == row1 || bad(row0, row1, before)) return;
   const int shift = __ffs(p.block) - 1;
   const int64_t blk = (before >> shift) + (blockIdx.x - item_start(p.cu, b, p.block));
   const int64_t base = blk << shift;               // position of the block's first token
@@ -182,13 +190,19 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(Kv8Read p) {
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  // starts that no row may lead to: a CTA behind those with rows looks at the whole batch
+  if (blockIdx.x == gridDim.x - 1 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < p.batch; i += blockDim.x)
+      if (bad_rows(__ldg(p.cu + i), __ldg(p.cu + i + 1), p.rows))
+        note_status(p.status, PIQ_ERR_INVALID_ARG, i);
   if (row >= p.rows) return;
   const int b = find_sequence(p.cu, p.batch, row, lane);
   if (b < 0) return;
-  const int64_t pos = __ldg(p.start + b) + (row - __ldg(p.cu + b));
+  const int64_t row0 = __ldg(p.cu + b), row1 = __ldg(p.cu + b + 1);
+  const int64_t pos = __ldg(p.start + b) + (row - row0);
   int64_t page = -1;
   const int shift = __ffs(p.block) - 1;
-  if (pos >= 0 && pos < p.width * p.block) page = __ldg(p.table + b * p.ldt + (pos >> shift));
+  if (pos >= 0 && pos < p.width * p.block && !bad_rows(row0, row1, p.rows)) page = __ldg(p.table + b * p.ldt + (pos >> shift));
   const bool bad = page < 0 || page >= p.pages;
   if (bad && lane == 0) note_status(p.status, PIQ_ERR_INVALID_ARG, b);
   const bool vals = blockIdx.y != 0;
@@ -236,7 +250,7 @@ int launch_append(const Kv8Write& p, cudaStream_t stream) {
   }
   const int64_t items = p.tokens / p.block + 2 * static_cast<int64_t>(p.batch);
   note_launch();
-  return launch_pdl(kern, dim3(static_cast<unsigned>(items), p.heads, 2), dim3(threads), 0, stream,
+  return launch_pdl(kern, dim3(static_cast<unsigned>(items + 1), p.heads, 2), dim3(threads), 0, stream,
                     p) == cudaSuccess
              ? PIQ_OK
              : PIQ_ERR_CUDA;
@@ -245,7 +259,7 @@ int launch_append(const Kv8Write& p, cudaStream_t stream) {
 template <typename T, int D>
 int launch_read(const Kv8Read& p, cudaStream_t stream) {
   note_launch();
-  return launch_pdl(kv8_read_kernel<T, D>, dim3(static_cast<unsigned>(ceil_div(p.rows, 8)), 2),
+  return launch_pdl(kv8_read_kernel<T, D>, dim3(static_cast<unsigned>(ceil_div(p.rows, 8) + 1), 2),
                     dim3(256), 0, stream, p) == cudaSuccess
              ? PIQ_OK
              : PIQ_ERR_CUDA;

@@ -131,7 +131,10 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
   const int64_t q0 = __ldg(p.cu + b), q1 = __ldg(p.cu + b + 1), seq_len = __ldg(p.lens + b);
   if (q0 == q1) return;
   T* out = static_cast<T*>(p.out);
-  if (bad_lengths<T, D>(p, b, q0, q1, seq_len, blockIdx.x == 0 && part == 0)) return;
+  if (bad_lengths(p, q0, q1, seq_len)) {
+    if (blockIdx.x == 0 && part == 0) report_lengths<T, D>(p, b, q0, q1);
+    return;
+  }
   const int n = static_cast<int>(q1 - q0), len = static_cast<int>(seq_len);
   const int rows = n * p.group;
   const int row0 = rg * ROWS;
@@ -581,9 +584,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv8_join_kernel(Kv8Attn p) {
   if (b < 0) return;
   const int64_t q0 = __ldg(p.cu + b), q1 = __ldg(p.cu + b + 1), len = __ldg(p.lens + b);
   const int64_t n = q1 - q0;
-  if (q0 < 0 || q1 > p.tokens || n > p.max_new || len < n || len > p.max_len ||
-      len > p.width * p.block)
-    return;  // its rows are NaN already
+  if (bad_lengths(p, q0, q1, len)) return;  // its rows are NaN already
   const int span = static_cast<int>(len) -
                    first_block_key(static_cast<int>(len), static_cast<int>(n), p.window, p.block);
   const int nc = (span + p.chunk - 1) / p.chunk;

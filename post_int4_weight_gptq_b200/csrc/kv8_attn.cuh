@@ -103,16 +103,16 @@ __device__ __forceinline__ float row_exponent<__nv_bfloat16>(float amax, float& 
   return __uint_as_float(e << 23);
 }
 
-// Whether sequence b's lengths cannot be; then status is set and its rows, as far
-// as they exist, are NaN (`writer`: this CTA does that).
-template <typename T, int D>
-__device__ __forceinline__ bool bad_lengths(const Kv8Attn& p, int b, int64_t q0, int64_t q1,
-                                            int64_t len, bool writer) {
+// Whether the lengths of a sequence (of any rows) cannot be.
+__device__ __forceinline__ bool bad_lengths(const Kv8Attn& p, int64_t q0, int64_t q1,
+                                            int64_t len) {
   const int64_t n = q1 - q0;
-  if (q0 >= 0 && n >= 0 && q1 <= p.tokens && n <= p.max_new && len >= n && len <= p.max_len &&
-      len <= p.width * p.block)
-    return false;
-  if (!writer) return true;
+  return bad_rows(q0, q1, p.tokens) ||
+         (n != 0 && (n > p.max_new || len < n || len > p.max_len || len > p.width * p.block));
+}
+// Then one CTA, all of it, sets the status and the rows, as far as they exist, to NaN.
+template <typename T, int D>
+__device__ __forceinline__ void report_lengths(const Kv8Attn& p, int b, int64_t q0, int64_t q1) {
   if (threadIdx.x == 0) note_status(p.status, PIQ_ERR_INVALID_ARG, b);
   const int64_t t0 = max(q0, static_cast<int64_t>(0)), t1 = min(q1, p.tokens);
   const float nan = __uint_as_float(0x7FC00000u);
@@ -122,7 +122,6 @@ __device__ __forceinline__ bool bad_lengths(const Kv8Attn& p, int b, int64_t q0,
     if (p.lse != nullptr)
       for (int i = threadIdx.x; i < p.heads; i += blockDim.x) p.lse[t * p.heads + i] = nan;
   }
-  return true;
 }
 
 // kv8_prompt.cu: the chunk kernel for many rows a kv head.

@@ -338,6 +338,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   pdl_wait();
+  // Bad lengths are found by the first CTA (whose item most often has no rows), over the
+  // whole batch: with starts that cannot be, the search below may pass a sequence by.
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    auto bad = [&](int i) {
+      return bad_lengths(p, __ldg(p.cu + i), __ldg(p.cu + i + 1), __ldg(p.lens + i));
+    };
+    bool any = false;
+    for (int i = threadIdx.x; i < p.batch; i += blockDim.x) any |= bad(i);
+    if (__syncthreads_or(any))
+      for (int i = 0; i < p.batch; ++i)
+        if (bad(i)) report_lengths<T, D>(p, i, __ldg(p.cu + i), __ldg(p.cu + i + 1));
+  }
   // ------------------------------------------------------------- which rows
   // Items of 256 rows are numbered without the lengths: sequence b's start at
   // floor(cu[b] group / 256) + b.  The last ones, which see most keys, go first.
@@ -367,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
   const int64_t q0 = __ldg(p.cu + b), q1 = __ldg(p.cu + b + 1), seq_len = __ldg(p.lens + b);
   if (q0 == q1) return;
   const int64_t first_row = (item - (q0 * p.group / kPromptRows + b)) * kPromptRows;
-  if (bad_lengths<T, D>(p, b, q0, q1, seq_len, first_row == 0 && part == 0 && kvh == 0)) return;
+  if (bad_lengths(p, q0, q1, seq_len)) return;
   const int n = static_cast<int>(q1 - q0), len = static_cast<int>(seq_len);
   const int rows = n * p.group;
   if (first_row >= rows) return;

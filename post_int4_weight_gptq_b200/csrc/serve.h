@@ -115,6 +115,11 @@ __device__ __forceinline__ void note_status(int32_t* status, int code, int detai
   if (atomicCAS(status, PIQ_OK, code) == PIQ_OK) status[1] = detail;
 }
 
+// Whether [row0, row1) cannot be a sequence's rows in a tensor of `rows` rows.
+__device__ __forceinline__ bool bad_rows(int64_t row0, int64_t row1, int64_t rows) {
+  return row0 != row1 && (row0 < 0 || row1 < row0 || row1 > rows);
+}
+
 // Eight consecutive values of one row, as they lie in memory and in fp32.
 template <typename T>
 struct Eight {

@@ -922,3 +922,59 @@ def test_a_wait_that_gives_up_leaves_nan(call, args):
     for g, w in zip(run(status), want):
         assert torch.equal(g, w)
     assert status.tolist() == [0, 0]
+
+
+# ------------------------------------------------------------------- bad row starts
+BAD_STARTS = [[-5000, 10], [-1, 4, 10], [10 ** 6, 10 ** 6 + 1], [0, 5, 3], [0, 4, 12],
+              [11, 12, 13], [0, 10, 2 ** 31 - 1, -2 ** 31], [-2 ** 31, -2 ** 31]]
+
+
+def bad_sequences(cu, rows):
+    return [i for i in range(len(cu) - 1)
+            if not 0 <= cu[i] <= cu[i + 1] <= rows and cu[i] != cu[i + 1]]
+
+
+@pytest.mark.parametrize("cu", BAD_STARTS)
+@pytest.mark.parametrize("heads", [2, 16, 200])
+def test_attention_bad_starts_are_reported(cu, heads):
+    # whatever the kernel (heads of 2 kv heads pick it) and wherever the rows would lie
+    rng = np.random.default_rng(heads)
+    n, bad = len(cu) - 1, bad_sequences(cu, 10)
+    b = Batch(rng, [60] * n, 2, 64, 16, BF16)
+    b.append([60] * n)
+    q = rand(rng, (10, heads, 64), BF16)
+    status, out = piq.new_status(), torch.full_like(q, 3.0)
+    _, lse = piq.kv8_attention(b.cache, q, ints(cu), ints(b.lens), b.gpu_table(), 10, 60,
+                               out=out, return_lse=True, status=status)
+    assert bool(bad) == (status.tolist()[0] == piq.PIQ_ERR_INVALID_ARG)
+    if bad:
+        assert status.tolist()[1] in bad
+    for i in bad:
+        rows = slice(max(cu[i], 0), max(min(cu[i + 1], 10), 0))
+        assert torch.isnan(out[rows]).all() and torch.isnan(lse[rows]).all()
+
+
+@pytest.mark.parametrize("cu", BAD_STARTS)
+def test_append_and_read_bad_starts_are_reported(cu):
+    rng = np.random.default_rng(1)
+    n, bad = len(cu) - 1, bad_sequences(cu, 10)
+    b = Batch(rng, [80] * n, 2, 64, 16, BF16)
+    b.append([40] * n)
+    kv = rand(rng, (10, 2, 64), BF16)
+    status, before = piq.new_status(), [t.clone() for t in b.cache]
+    piq.kv8_append(b.cache, kv, kv, ints(cu), ints(b.lens), b.gpu_table(), status=status)
+    assert bool(bad) == (status.tolist()[0] == piq.PIQ_ERR_INVALID_ARG)
+    for i in bad:                                  # their pages are as they were
+        assert status.tolist()[1] in bad
+        for x, y in zip(before, b.cache):
+            p = torch.from_numpy(b.table[i].copy()).cuda()
+            assert torch.equal(x[p].view(torch.int8), y[p].view(torch.int8))
+    status.zero_()
+    out = tuple(torch.full((10, 2, 64), 3.0, dtype=BF16, device="cuda") for _ in range(2))
+    piq.kv8_read(b.cache, ints(cu), ints([0] * n), b.gpu_table(), 10, BF16, out=out,
+                 status=status)
+    assert bool(bad) == (status.tolist()[0] == piq.PIQ_ERR_INVALID_ARG)
+    for i in bad:
+        assert status.tolist()[1] in bad
+        for o in out:
+            assert torch.isnan(o[max(cu[i], 0):max(min(cu[i + 1], 10), 0)]).all()
