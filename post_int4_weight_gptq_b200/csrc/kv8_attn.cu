@@ -578,8 +578,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv8_join_kernel(Kv8Attn p) {
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t = blockIdx.x;
-  const int head = blockIdx.y;
+  const int64_t t = blockIdx.x / static_cast<unsigned>(p.heads);
+  const int head = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.heads));
   const int b = find_sequence(p.cu, p.batch, t, lane);
   if (b < 0) return;
   const int64_t q0 = __ldg(p.cu + b), q1 = __ldg(p.cu + b + 1), len = __ldg(p.lens + b);
@@ -700,7 +700,7 @@ bool attn_sizes_ok(int64_t tokens, int heads, int kv_heads, int head_dim, int64_
                    int64_t max_new, int64_t max_len, int window) {
   return tokens >= 0 && tokens <= (int64_t)1 << 24 && kv_heads >= 1 && kv_heads <= 1024 &&
          heads >= kv_heads && heads % kv_heads == 0 && heads / kv_heads <= 256 &&
-         heads <= 65535 && tokens * heads <= INT32_MAX - 256 &&
+         tokens * heads <= INT32_MAX - 256 &&
          (head_dim == 64 || head_dim == 128) && batch >= 1 && batch <= 65535 && max_new >= 0 &&
          max_new <= INT32_MAX && max_len >= 0 && max_len <= (int64_t)1 << 26 && window >= 0;
 }
@@ -736,7 +736,7 @@ bool page_map(CUtensorMap* map, const int8_t* codes, const Kv8Attn& p) {
 template <typename T, int D>
 int launch_join(const Kv8Attn& p, cudaStream_t stream) {
   note_launch();
-  return launch_pdl(kv8_join_kernel<T, D>, dim3(static_cast<unsigned>(p.tokens), p.heads),
+  return launch_pdl(kv8_join_kernel<T, D>, dim3(static_cast<unsigned>(p.tokens * p.heads)),
                     dim3(32 * kJoinWarps), 0, stream, p) == cudaSuccess
              ? PIQ_OK
              : PIQ_ERR_CUDA;

@@ -978,3 +978,28 @@ def test_append_and_read_bad_starts_are_reported(cu):
         assert status.tolist()[1] in bad
         for o in out:
             assert torch.isnan(o[max(cu[i], 0):max(min(cu[i + 1], 10), 0)]).all()
+
+
+# ----------------------------------------------------------------------- many heads
+@pytest.mark.parametrize("max_len", [40, 100000])
+def test_attention_more_heads_than_a_grid_dimension(max_len):
+    kvh, group, dim, n = 1024, 65, 64, 20
+    g = torch.Generator(device="cuda").manual_seed(5)
+    cache = piq.kv8_cache(3, kvh, dim, 16)
+    k, v = (torch.randn(n, kvh, dim, generator=g, device="cuda") for _ in range(2))
+    table = ints([[2, 0]])
+    piq.kv8_append(cache, k, v, ints([0, n]), ints([0]), table)
+    q = torch.randn(1, kvh * group, dim, generator=g, device="cuda").to(BF16)
+    out, lse = piq.kv8_attention(cache, q, ints([0, 1]), ints([n]), table, 1, max_len,
+                                 return_lse=True)
+    kk, vv = (x.double() for x in piq.kv8_read(cache, ints([0, n]), ints([0]), table, n, FP32))
+    s = torch.einsum("hgd,nhd->hgn", q[0].view(kvh, group, dim).double(), kk) * dim ** -0.5
+    p = torch.softmax(s, 2)
+    ref = torch.einsum("hgn,nhd->hgd", p, vv).view(1, -1, dim)
+    size = torch.einsum("hgn,nhd->hgd", p, vv.abs()).view(1, -1, dim)
+    # the roundings of the weights (2^-11 each) and of the result; the scores' (d + 4) 2^-23 of
+    # their sums of magnitudes, which are below 2^7 here, twice, and the exponential's 2^-20
+    off = 2 * (dim + 4) * 2.0 ** -23 * 2 ** 7 + 2.0 ** -20
+    tol = size * (2.0 ** -11 + 2 * off) + ref.abs() * half_step(BF16) * 1.01 + 2.0 ** -25
+    assert ((out.double() - ref).abs() <= tol).all()
+    assert ((lse[0].double() - torch.logsumexp(s, 2).view(-1)).abs() <= off + 2.0 ** -18).all()

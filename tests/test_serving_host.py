@@ -215,3 +215,12 @@ def test_wait_limit(lib):
     assert lib.piq_serving_wait_limit(10 ** 10 + 1) == piq.PIQ_ERR_INVALID_ARG
     for ns in (1, 10 ** 10, 0):
         piq.serving_wait_limit(ns)
+
+
+def test_attention_heads_up_to_the_limit(lib):
+    assert piq.kv8_attention_workspace_bytes(1, 256 * 1024, 1024, 64, 1, 1, 1000) >= 256
+    assert piq.kv8_attention_workspace_bytes(4, 65536, 1024, 128, 3, 2, 100000) >= 256
+    with pytest.raises(piq.PiqError):
+        piq.kv8_attention_workspace_bytes(1, 257 * 1024, 1024, 64, 1, 1, 1000)
+    with pytest.raises(piq.PiqError):   # tokens * heads
+        piq.kv8_attention_workspace_bytes(1 << 13, 256 * 1024, 1024, 64, 1, 1, 1000)
