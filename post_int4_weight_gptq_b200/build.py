@@ -4,7 +4,8 @@ kernels and the C ABI, sm_100a) and ``lib/piq_serve.so`` (the Python entry of th
 
 Usage: ``python -m post_int4_weight_gptq_b200.build [--force] [--verbose]``.
 Sources are ``csrc/*.cu``; the C ABI is ``include/piq.h`` at the repository
-root.  Objects are rebuilt when a source or header is newer than the library.
+root.  Objects are rebuilt when a source or header is newer than the library, the
+binding also when Python or torch has changed.
 """
 from __future__ import annotations
 
@@ -25,6 +26,7 @@ OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(LIBDIR, "libpiq.so")
 SERVE = os.path.join(LIBDIR, "piq_serve.so")
 SERVE_SRC = os.path.join(CSRC, "serve_binding.cpp")
+SERVE_FOR = os.path.join(OBJDIR, "piq_serve.for")  # what piq_serve.so was built for
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -55,11 +57,28 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def _serve_for() -> str:
+    """The Python and torch whose headers and libraries the binding is built against."""
+    import torch
+    return (f"python {sys.version}\ntorch {torch.__version__} {torch.version.git_version} "
+            f"cxx11abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)}\n")
+
+
+def serve_up_to_date() -> bool:
+    if not os.path.exists(SERVE) or any(
+            os.path.getmtime(p) > os.path.getmtime(SERVE)
+            for p in (SERVE_SRC, os.path.join(INCLUDE, "piq.h"))):
+        return False
+    try:
+        with open(SERVE_FOR) as f:
+            return f.read() == _serve_for()
+    except OSError:
+        return False
+
+
 def build_serve(force: bool = False) -> str:
     """The serving binding; needs libpiq.so to link to."""
-    if not force and os.path.exists(SERVE) and all(
-            os.path.getmtime(p) <= os.path.getmtime(SERVE)
-            for p in (SERVE_SRC, os.path.join(INCLUDE, "piq.h"))):
+    if not force and serve_up_to_date():
         return SERVE
     import torch
     base = os.path.dirname(torch.__file__)
@@ -76,6 +95,9 @@ def build_serve(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {os.path.basename(SERVE_SRC)}:\n{r.stderr}")
     os.replace(tmp, SERVE)
+    os.makedirs(OBJDIR, exist_ok=True)
+    with open(SERVE_FOR, "w") as f:
+        f.write(_serve_for())
     return SERVE
 
 

@@ -224,3 +224,32 @@ def test_attention_heads_up_to_the_limit(lib):
         piq.kv8_attention_workspace_bytes(1, 257 * 1024, 1024, 64, 1, 1, 1000)
     with pytest.raises(piq.PiqError):   # tokens * heads
         piq.kv8_attention_workspace_bytes(1 << 13, 256 * 1024, 1024, 64, 1, 1, 1000)
+
+
+def test_binding_is_rebuilt_for_another_torch_or_python(monkeypatch, tmp_path):
+    import subprocess
+    built = []
+
+    def compile_(cmd, **kw):
+        built.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("binding")
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(piq_build.subprocess, "run", compile_)
+    monkeypatch.setattr(piq_build, "SERVE", str(tmp_path / "piq_serve.so"))
+    monkeypatch.setattr(piq_build, "OBJDIR", str(tmp_path / "obj"))
+    monkeypatch.setattr(piq_build, "SERVE_FOR", str(tmp_path / "obj" / "piq_serve.for"))
+    piq_build.build_serve()
+    piq_build.build_serve()
+    assert len(built) == 1
+    monkeypatch.setattr(torch, "__version__", "9.9.9")
+    piq_build.build_serve()
+    piq_build.build_serve()
+    assert len(built) == 2
+    monkeypatch.setattr(piq_build.sys, "version", "4.0")
+    piq_build.build_serve()
+    assert len(built) == 3
+    (tmp_path / "obj" / "piq_serve.for").unlink()    # nobody knows what it was built for
+    piq_build.build_serve()
+    assert len(built) == 4
