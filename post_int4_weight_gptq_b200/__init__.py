@@ -554,8 +554,10 @@ def new_status(device=None):
 
 
 def check_status(status, where="8-bit call"):
-    """Raises PiqError if an entry recorded an error in `status` (synchronizes),
-    and clears it."""
+    """Raises PiqError if an entry recorded an error in `status` (synchronizes with
+    the device, whatever streams the calls were made on), and clears it."""
+    if status.is_cuda:
+        torch.cuda.synchronize(status.device)
     code = int(status[0])
     if code != PIQ_OK:
         status.zero_()

@@ -1003,3 +1003,22 @@ def test_attention_more_heads_than_a_grid_dimension(max_len):
     tol = size * (2.0 ** -11 + 2 * off) + ref.abs() * half_step(BF16) * 1.01 + 2.0 ** -25
     assert ((out.double() - ref).abs() <= tol).all()
     assert ((lse[0].double() - torch.logsumexp(s, 2).view(-1)).abs() <= off + 2.0 ** -18).all()
+
+
+def test_check_status_waits_for_every_stream():
+    rng = np.random.default_rng(26)
+    b = Batch(rng, [40], 2, 64, 16, BF16)
+    b.append([20])
+    status, kv = piq.new_status(), rand(rng, (1, 2, 64), BF16)
+    cu, lens, table = ints([0, 1]), ints([20]), b.gpu_table().clone()
+    table[0, 1] = 10 ** 6
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(2):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(50_000_000)            # some 30 ms ahead of the call
+        piq.kv8_append(b.cache, kv, kv, cu, lens, table, stream=side, status=status)
+        with pytest.raises(piq.PiqError):
+            piq.check_status(status)
+        torch.cuda.synchronize()
+        assert status.tolist() == [0, 0]
