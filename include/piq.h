@@ -478,14 +478,16 @@ int piq_kv8_read(const int8_t* k_codes, const int8_t* v_codes, const float* k_sc
  * query at position p sees keys j <= p, and j > p - window when window > 0:
  *   out = sum_j softmax_j(scale q . (k_scale k_j)) v_scale v_j,
  *   lse = log sum_j exp(scale q . (k_scale k_j)).
- * A query that sees no key gets out = 0 and lse = -infinity.
+ * A query that sees no key gets out = 0 and lse = -infinity, one whose row holds
+ * an infinity or NaN gets NaN for both.
  *   q, out  device [tokens, heads, head_dim], bf16 or fp16, token strides ldq
  *           and ldo (multiples of 8), 16-byte aligned.
  *   lse     device fp32 [tokens, heads] or NULL.
  *   max_new, max_len   host upper bounds of the new tokens and of lens over the
  *           batch: they size the launch and the workspace (a sequence above
  *           them is an error: its rows are NaN).
- *           max_len <= 2^26.
+ *           max_len <= 2^26.  The keys are split over CTAs by max_len, whatever the
+ *           lengths: a bound far above them costs time and workspace.
  *   scale   |scale| <= 2^127.
  *   heads   a multiple of kv_heads, at most 256 kv_heads; tokens <= 2^24 and
  *           tokens * heads < 2^31 - 256.

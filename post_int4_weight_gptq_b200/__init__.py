@@ -585,7 +585,7 @@ def int8_linear(X, W, w_scale, bias=None, out=None, stream=None, workspace=None,
     """X W^T + bias on int8 codes: the tokens X [tokens, in] (bf16, fp16, fp32)
     are quantized inside the call, W [out, in] int8 and w_scale fp32 [out] are
     int8_quantize_rows of the weight (row stride a multiple of 16), bias is fp32
-    [out].  The result has X's dtype."""
+    [out].  The result has X's dtype and no gradient."""
     return (_serve or _serving()).int8_linear(X, W, w_scale, bias, out, _handle(stream),
                                               workspace, status)
 
@@ -637,7 +637,9 @@ def kv8_attention(cache, q, cu, lens, block_table, max_new, max_len, scale=None,
     cached tokens (appended before this call).  max_new and max_len bound the
     rows and lens of every sequence; scale defaults to head_dim ** -0.5; window
     > 0 limits a query to the last `window` keys.  Returns out, or (out, lse)
-    with lse fp32 [tokens, heads]."""
+    with lse fp32 [tokens, heads], without gradients.  Rows of no sequence are left
+    as they are (`out`) or undefined.  max_len also decides how the keys are split:
+    near the longest sequence is the fastest."""
     return (_serve or _serving()).kv8_attention(
         *cache, q, cu, lens, block_table, max_new, max_len, scale, window, return_lse, out,
         _handle(stream), workspace, status)

@@ -398,7 +398,8 @@ __device__ __forceinline__ void umma_commit_pair_here(uint64_t* bar) {
 }
 // `bytes` that no copy will bring are taken off the current phase of `bar`.
 __device__ __forceinline__ void mbar_forgo_tx(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+  asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(
+                   smem_u32(bar)),
                "r"(bytes)
                : "memory");
 }

@@ -202,7 +202,8 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(Kv8Read p) {
   const int64_t pos = __ldg(p.start + b) + (row - row0);
   int64_t page = -1;
   const int shift = __ffs(p.block) - 1;
-  if (pos >= 0 && pos < p.width * p.block && !bad_rows(row0, row1, p.rows)) page = __ldg(p.table + b * p.ldt + (pos >> shift));
+  if (pos >= 0 && pos < p.width * p.block && !bad_rows(row0, row1, p.rows))
+    page = __ldg(p.table + b * p.ldt + (pos >> shift));
   const bool bad = page < 0 || page >= p.pages;
   if (bad && lane == 0) note_status(p.status, PIQ_ERR_INVALID_ARG, b);
   const bool vals = blockIdx.y != 0;
@@ -250,8 +251,8 @@ int launch_append(const Kv8Write& p, cudaStream_t stream) {
   }
   const int64_t items = p.tokens / p.block + 2 * static_cast<int64_t>(p.batch);
   note_launch();
-  return launch_pdl(kern, dim3(static_cast<unsigned>(items + 1), p.heads, 2), dim3(threads), 0, stream,
-                    p) == cudaSuccess
+  return launch_pdl(kern, dim3(static_cast<unsigned>(items + 1), p.heads, 2), dim3(threads), 0,
+                    stream, p) == cudaSuccess
              ? PIQ_OK
              : PIQ_ERR_CUDA;
 }

@@ -42,7 +42,7 @@ constexpr int kWarps = 6;
 // Bytes of a warp's ring: two stages of 32 keys and values.
 constexpr int ring_bytes(int dim) { return 2 * 64 * dim; }
 // CTAs that share a multiprocessor, as their registers allow (three of 64 dimensions
-// and one group of rows instead of two: 70 -> 63 us on 48 ragged sequences).
+// and one group of rows instead of two: 67.9 -> 64.1 us on 48 ragged sequences).
 constexpr int ctas_sm(int dim, int nt) { return (dim == 64 ? 4 : 3) - nt; }
 constexpr int kMaxPages = 256;        // pages of a chunk (4096 keys, blocks of 16)
 
@@ -270,7 +270,8 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_sm(D, NT)) kv8_chunk_kernel(
       hi[t][e] = row < rows ? len - n + tok + 1 - k0 : 0;
     }
   }
-  // tiles in which every row sees every key need no masks
+  // Tiles in which every row sees every key need no masks.  (Rows that do not exist see
+  // none, so that a group of fewer than eight rows masks every step.)
   const unsigned last_tok = static_cast<unsigned>(min(row0 + ROWS, rows) - 1) / p.group;
   const unsigned first_tok = static_cast<unsigned>(row0) / p.group;
   const int all_lo =
@@ -652,10 +653,10 @@ constexpr int64_t kMinChunk = 256, kManyCtasChunk = 2048, kMaxChunk = 4096;
 constexpr int64_t kMinPromptChunk = 512;
 // Rows a kv head above which the tensor-memory kernel runs.  Groups of 16 rows here each
 // read the codes again, mostly from L2; there the time hardly depends on the rows.
-// Here and there in us, 8 sequences of 4096 keys and 8 kv heads: dim 128, 16 rows 29.5
-// and 58.7, 32 rows 53.1 and 66.5, 48 rows 76 and 70; dim 64, 32 rows 29 and 55, 48 rows
-// 46 and 58.  48 such sequences: dim 128, 32 rows 281 and 289, 48 rows 406 and 289;
-// dim 64, 48 rows 208 and 250.
+// Here and there in us, 8 sequences of 4096 keys and 8 kv heads: dim 128, 16 rows 28.9
+// and 61.1, 32 rows 50.9 and 63.2, 48 rows 73.4 and 67.1; dim 64, 32 rows 27.9 and 52.6,
+// 48 rows 43.7 and 55.9.  48 such sequences: dim 128, 32 rows 267 and 287, 48 rows 385 and
+// 291; dim 64, 48 rows 197 and 249.
 constexpr int64_t many_rows(int dim) { return dim == 64 ? 48 : 32; }
 
 struct AttnPlan {

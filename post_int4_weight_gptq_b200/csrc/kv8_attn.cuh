@@ -39,8 +39,8 @@ constexpr float kSlack = 7.0f;        // log2 by which a score may pass the maxi
 // The weights of the values enter the second product in fp16 as 2^(x - m) v_scale c.
 // c = 2^(7 - d) is a row's own: 2^d is the power of two at or below the largest v_scale
 // of the blocks that the row has seen keys of, so that what a row does not see takes no
-// bits from it (and changes none of them).  d is at least -119 and c a normal number;
-// with scores up to kSlack above the maximum a weight stays below 2^15.
+// bits from it.  d is at least -119 and c a normal number; with scores up to kSlack above
+// the maximum a weight stays below 2^15.
 constexpr float kFirstFactor = 0x1p126f;
 constexpr float kWide = 256.0f;  // v_scale c from which c has to move
 

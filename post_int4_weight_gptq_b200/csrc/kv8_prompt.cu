@@ -11,9 +11,9 @@
 //
 // with the running maximum m moved, and O rescaled, only when a score passes it
 // by 2^7.  c is 2^7 over the largest value scale that the row has seen (a power of
-// two, moved like m); the sum of 2^(x - m) is fp32.  The codes are widened to fp16 as they come from
-// the pages (no second copy of the cache exists): bytes go through registers to
-// the swizzled tiles both products read.
+// two, moved like m); the sum of 2^(x - m) is fp32.  The codes are widened to fp16
+// as they come from the pages (no second copy of the cache exists): bytes go through
+// registers to the swizzled tiles both products read.
 //
 // 16 warps: 0 - 3 and 4 - 7 the softmax of tile 0 and 1 (a row a thread),
 // 8 - 11 widen keys and values, 12 issues the MMAs (13 - 15 only give their
@@ -445,7 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
         }
         umma_commit(&sh.s_full[t]);
       };
-      bool ok = wait_bar(&sh.q_full, 0, p.wait_ns, p.status, 70) && wait_bar(&sh.k_full[0], 0, p.wait_ns, p.status, 71);
+      bool ok = wait_bar(&sh.q_full, 0, p.wait_ns, p.status, 70) &&
+                wait_bar(&sh.k_full[0], 0, p.wait_ns, p.status, 71);
       const bool began = ok;
       if (ok) {
         tc_fence_after();
@@ -456,7 +457,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(Kv8Attn p) {
         const int st = j & 1;
         if (!(ok = wait_bar(&sh.v_full[st], (j >> 1) & 1, p.wait_ns, p.status, 72))) break;
         const bool more = j + 1 < nt;
-        if (more && !(ok = wait_bar(&sh.k_full[st ^ 1], ((j + 1) >> 1) & 1, p.wait_ns, p.status, 73))) break;
+        if (more &&
+            !(ok = wait_bar(&sh.k_full[st ^ 1], ((j + 1) >> 1) & 1, p.wait_ns, p.status, 73)))
+          break;
         for (int t = 0; t < nq; ++t) {
           if (!(ok = wait_bar(&sh.p_full[t], j & 1, p.wait_ns, p.status, 74))) break;
           tc_fence_after();
